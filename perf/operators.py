@@ -258,9 +258,6 @@ def prepare(case, seed):
         s["mp"] = torch.where(pick[:, 2] > 0, 0.1 * r[:, 3], torch.zeros(rows, **f32))
         s["idx"] = torch.empty(rows, dtype=torch.int32, device=DEV)
         s["lp"] = torch.empty(rows, **f32)
-        if own:
-            import block_attention_b200 as ba
-            s["ws"] = ba.Workspace(DEV)
     return s
 
 
@@ -374,7 +371,7 @@ def run(state):
                                        s["table"], s["ctx"], mode, shared_prefix=c["prefix"],
                                        max_ctx=max(s["lens"]), out=s["out"], workspace=s["ws"])
         ba.vocab_sample_filtered(s["x"], s["u"], temperature=s["T"], top_k=s["k"], top_p=s["p"],
-                                 min_p=s["mp"], idx=s["idx"], logprob=s["lp"], workspace=s["ws"])
+                                 min_p=s["mp"], idx=s["idx"], logprob=s["lp"])
         return s["idx"], s["lp"]
     if c["op"] == "rope":
         s["out"].copy_(_rotate(s["x"], s["pos"], s["freq"], s["m"], c["layout"], c["inverse"]))
