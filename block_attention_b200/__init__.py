@@ -11,6 +11,10 @@ Entry points (same names as the C ABI, minus the ``orthrus_`` prefix):
     vocab_argmax    per-row argmax, lowest index on ties
     consensus       accepted prefix, tokens to emit, next anchor
     kv_commit       copy accepted block K/V rows into every layer's cache
+the paged cache of ``include/orthrus_paged.h``:
+    rope            rotary positions: layouts, part of a head, scaled frequencies
+    paged_append    K/V rows into pages, rotated on the way
+    paged_block_attn  the views' attention over pages, shared prefixes read once
 and the row-invariant decoder building blocks of ``include/orthrus_decoder.h``
 (embed, rmsnorm, linear, qkv_rope, swiglu, block_tokens) that
 ``block_attention_b200.decoder`` composes into the end-to-end consensus loop.
@@ -78,6 +82,65 @@ class SampleArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class FilterArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("rows", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("row_stride", ctypes.c_int64), ("logits", ctypes.c_void_p),
+                ("u", ctypes.c_void_p), ("temperature", ctypes.c_void_p),
+                ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("idx", ctypes.c_void_p),
+                ("logprob", ctypes.c_void_p), ("err", ctypes.c_void_p)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original_ctx", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("mscale", ctypes.c_double)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("D", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("mscale", ctypes.c_double),
+                ("x", ctypes.c_void_p), ("x_row_stride", ctypes.c_int64),
+                ("x_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p)]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layers", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("blk", ctypes.c_int32), ("rows", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("advance", ctypes.c_int32), ("mscale", ctypes.c_double),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("k_layer_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_layer_stride", ctypes.c_int64),
+                ("v_row_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("pages_layer_stride", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p),
+                ("n_rows", ctypes.c_void_p), ("row_starts", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("err", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("mask_mode", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("blk", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_ctx", ctypes.c_int32), ("shared_prefix", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("k_blk", ctypes.c_void_p),
+                ("v_blk", ctypes.c_void_p), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("ctx_lens", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("err", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 EXPORTS = ("orthrus_block_attn", "orthrus_block_attn_workspace",
            "orthrus_block_attn_launches", "orthrus_block_attn_plan", "orthrus_vocab_argmax",
            "orthrus_vocab_argmax_workspace", "orthrus_consensus", "orthrus_kv_commit",
@@ -87,6 +150,11 @@ EXPORTS = ("orthrus_block_attn", "orthrus_block_attn_workspace",
            "orthrus_lm_head_argmax", "orthrus_lm_head_argmax_workspace",
            "orthrus_lm_head_argmax_plan",
            "orthrus_linear_tc", "orthrus_linear_tc_workspace", "orthrus_linear_tc_plan",
+           "orthrus_vocab_sample_filtered",
+           # paged cache (include/orthrus_paged.h)
+           "orthrus_rope_freqs", "orthrus_rope", "orthrus_paged_append",
+           "orthrus_paged_append_workspace", "orthrus_paged_attn",
+           "orthrus_paged_attn_workspace",
            "orthrus_rope_table", "orthrus_linear_tc_qkv_rope", "orthrus_selftest_bounded_wait",
            # decoder building blocks (include/orthrus_decoder.h)
            "orthrus_embed", "orthrus_rmsnorm", "orthrus_linear", "orthrus_qkv_rope",
@@ -154,6 +222,15 @@ def lib() -> ctypes.CDLL:
         L.orthrus_lm_head_argmax_workspace.restype = sz
         L.orthrus_lm_head_argmax.argtypes = [i32, vp, i32, i32, i64, vp, i32, vp, vp, vp, vp,
                                              sz, vp]
+        L.orthrus_vocab_sample_filtered.argtypes = [c.POINTER(FilterArgs), vp]
+        L.orthrus_rope_freqs.argtypes = [i32, c.c_double, c.POINTER(RopeScaling), vp, vp]
+        L.orthrus_rope.argtypes = [c.POINTER(RopeArgs), vp]
+        L.orthrus_paged_append.argtypes = [c.POINTER(AppendArgs), vp]
+        L.orthrus_paged_append_workspace.argtypes = [c.POINTER(AppendArgs)]
+        L.orthrus_paged_append_workspace.restype = sz
+        L.orthrus_paged_attn.argtypes = [c.POINTER(PagedAttnArgs), vp]
+        L.orthrus_paged_attn_workspace.argtypes = [c.POINTER(PagedAttnArgs)]
+        L.orthrus_paged_attn_workspace.restype = sz
         _lib = L
     return _lib
 
@@ -577,3 +654,302 @@ def linear_tc(x, w, *, residual=None, out=None, l2_next=None, err=None, workspac
         _dtype(x), _ptr(x), rows, K, x.stride(0), _ptr(w), N, _ptr(residual), _ptr(out),
         out.stride(0), hp, hb, _ptr(err), _ptr(buf), buf.numel(), _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------- paged cache
+
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALINGS = {"linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+def _like(name, t, dtype, device, shape=None):
+    """Refuse a tensor of another type, device or shape (None: not given)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+
+
+def _on(device, stream):
+    """Context in which a call launches and allocates: the tensors' device, and
+    the given stream if there is one."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(device)
+
+
+class _StreamWorkspace(Workspace):
+    """Default scratch of one operator on one stream: calls on other streams
+    use other buffers, and an outgrown buffer lives on, for a captured graph
+    may still name it (sizes at least double, so they add up to little)."""
+
+    def __init__(self, device):
+        super().__init__(device)
+        self.outgrown = []
+
+    def get(self, nbytes: int) -> torch.Tensor:
+        if self.buf.numel() < nbytes:
+            if self.buf.numel():
+                self.outgrown.append(self.buf)
+            nbytes = max(nbytes, 2 * self.buf.numel(), 256)
+            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        return self.buf
+
+
+def _stream_ws(ws, device, op):
+    """Caller's workspace, else the current stream's default for this op."""
+    if ws is None:
+        key = (device.index, op, torch.cuda.current_stream(device).cuda_stream)
+        ws = _default_ws.get(key)
+        if ws is None:
+            ws = _default_ws[key] = _StreamWorkspace(device)
+    return ws
+
+
+def rope_freqs(rot, theta, *, scaling=None, factor=1.0, original_ctx=0.0, low=1.0, high=0.0,
+               mscale=0.0, device="cuda"):
+    """(inv_freq float64 [rot/2] on ``device``, mscale) for rope and
+    paged_append: theta^(-2i/rot), scaled for long contexts by ``scaling`` =
+    "linear", "ntk", "bands" or "yarn" (see orthrus_paged.h; ``low`` / ``high``
+    default to 1 / 4 turns for bands, 1 / 32 for YaRN)."""
+    if scaling is not None and scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be None or one of {sorted(ROPE_SCALINGS)}")
+    kind = ROPE_SCALINGS.get(scaling, 0)
+    if high == 0.0:
+        high = 4.0 if scaling == "bands" else 32.0
+    s = RopeScaling(kind, factor, original_ctx, low, high, mscale)
+    f = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
+    m = ctypes.c_double(0.0)
+    _check("orthrus_rope_freqs", lib().orthrus_rope_freqs(
+        int(rot), float(theta), ctypes.byref(s), ctypes.c_void_p(f.data_ptr()),
+        ctypes.byref(m)))
+    return f.to(device), m.value
+
+
+def _rot(inv_freq, device):
+    if inv_freq is None:
+        return 0
+    _like("inv_freq", inv_freq, torch.float64, device)
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous vector")
+    return 2 * inv_freq.numel()
+
+
+def rope(x, positions, inv_freq, *, layout=ROPE_HALF, mscale=1.0, inverse=False, out=None,
+         stream=None):
+    """Rotary embedding of x [rows, H, D] at positions int32 [rows]: the first
+    2 * inv_freq.numel() values of each head are turned by pos * inv_freq
+    (float64, rope_freqs) and scaled by mscale, the others copied.  x and out
+    may be views with any row and head strides (unit stride inside a head);
+    ``out=x`` rotates in place.  ``inverse`` turns back: the gradient with
+    respect to x of the call with the same arguments."""
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a CUDA device (no CPU path)")
+    if x.dim() != 3 or (x.numel() and x.stride(2) != 1):
+        raise ValueError("x must be [rows, H, D] with unit stride inside a head")
+    rows, H, D = x.shape
+    _like("positions", positions, torch.int32, x.device, (rows,))
+    _dev(positions)
+    if out is not None:
+        _like("out", out, x.dtype, x.device, x.shape)
+        if out.numel() and out.stride(2) != 1:
+            raise ValueError("out must have unit stride inside a head")
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty(rows, H, D, dtype=x.dtype, device=x.device)
+        a = RopeArgs(_dtype(x), int(layout), rows, H, D, _rot(inv_freq, x.device),
+                     int(bool(inverse)), float(mscale), x.data_ptr(), x.stride(0), x.stride(1),
+                     out.data_ptr(), out.stride(0), out.stride(1), positions.data_ptr(),
+                     None if inv_freq is None else inv_freq.data_ptr())
+        _check("orthrus_rope", lib().orthrus_rope(ctypes.byref(a), _stream(stream)))
+    return out
+
+
+def paged_append(k, v, k_pages, v_pages, page_table, ctx_lens, *, n_rows=None, row_starts=None,
+                 inv_freq=None, layout=ROPE_HALF, mscale=1.0, q=None, q_out=None, advance=False,
+                 err=None, workspace=None, stream=None):
+    """Write K/V rows into pages [pages, Hkv, page_size, D] at positions
+    ctx_lens[b] + j, K rotated on the way when ``inv_freq`` is given, and q's
+    rows rotated to their positions into q_out (see orthrus_paged.h).
+
+    Blocks: k, v [B, blk, Hkv, D] (q [B, blk, Hq, D]), of which the first
+    n_rows[b] rows are taken (default: all); with a leading layer dimension on
+    k, v and both pools, all layers in one call.  Ragged: k, v [rows, Hkv, D]
+    (q [rows, Hq, D]) and row_starts int32 [B + 1].  Rows may be strided views
+    of one projection's output.  ``advance`` adds the rows taken to ctx_lens.
+    Returns q_out (None without q)."""
+    if not k.is_cuda:
+        raise ValueError("tensors must be on a CUDA device (no CPU path)")
+    dev, dt = k.device, k.dtype
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, max_pages = page_table.shape
+    _like("page_table", page_table, torch.int32, dev)
+    _like("ctx_lens", ctx_lens, torch.int32, dev, (B,))
+    _like("n_rows", n_rows, torch.int32, dev, (B,))
+    _like("row_starts", row_starts, torch.int32, dev, (B + 1,))
+    _like("err", err, torch.int32, dev)
+    for name, t in (("v", v), ("k_pages", k_pages), ("v_pages", v_pages)):
+        _like(name, t, dt, dev)
+    _dev(page_table, ctx_lens, n_rows, row_starts, err, q_out)
+    block_dims = 3 if row_starts is not None else 4
+    layered = k.dim() == block_dims + 1
+    if k.dim() != block_dims + layered or v.shape != k.shape:
+        raise ValueError("k and v must be [B, blk, Hkv, D], or [rows, Hkv, D] with row_starts, "
+                         "with an optional leading layer dimension")
+    if k_pages.dim() != 4 + layered or k_pages.shape != v_pages.shape \
+            or k_pages.stride() != v_pages.stride():
+        raise ValueError("k_pages and v_pages must be laid out alike, [pages, Hkv, page_size, D] "
+                         "with k's layer dimension")
+    if layered:
+        layers = k.shape[0]
+        if k_pages.shape[0] != layers or not (k_pages[:1].is_contiguous()):
+            raise ValueError("the pools must hold k's layers, each contiguous")
+        pages_stride = k_pages.stride(0)
+    else:
+        layers, pages_stride = 1, 0
+        if not k_pages.is_contiguous():
+            raise ValueError("the pools must be contiguous")
+    pages, Hkv, page_size, D = k_pages.shape[-4:]
+    if k.shape[-2:] != (Hkv, D):
+        raise ValueError("k and the pools disagree on Hkv or D")
+
+    def strides(t, name):
+        """(layer, row, head) strides of t's rows."""
+        if t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have unit stride inside a head")
+        if row_starts is None:
+            if t.shape[-4] != B:
+                raise ValueError(f"{name} and page_table disagree on B")
+            if t.shape[-4] > 1 and t.shape[-3] > 1 and t.stride(-4) != t.shape[-3] * t.stride(-3):
+                raise ValueError(f"{name}: the rows of consecutive blocks must be evenly spaced")
+            row = t.stride(-3) if t.shape[-3] > 1 else t.stride(-4)
+        else:
+            row = t.stride(-3)
+        return (t.stride(0) if layered else 0), row, t.stride(-2)
+
+    ks, vs = strides(k, "k"), strides(v, "v")
+    blk = k.shape[-3] if row_starts is None else 0
+    rows = k.shape[-3] if row_starts is not None else B * blk
+    Hq, qs = 0, (0, 0, 0)
+    if q is not None:
+        if layered or q.dim() != block_dims or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != D:
+            raise ValueError("q must be shaped like k but for its heads, without layers")
+        _like("q", q, dt, dev)
+        Hq, qs = q.shape[-2], strides(q, "q")
+        _like("q_out", q_out, dt, dev, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    with _on(dev, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=dev)
+        a = AppendArgs(_dtype(k), layers, B, blk, rows, Hq, Hkv, D, page_size, pages, max_pages,
+                       _rot(inv_freq, dev), int(layout), int(bool(advance)), float(mscale),
+                       k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(), *ks, *vs,
+                       qs[1], qs[2], None if q is None else q_out.data_ptr(), k_pages.data_ptr(),
+                       v_pages.data_ptr(), pages_stride, page_table.data_ptr(), ctx_lens.data_ptr(),
+                       None if n_rows is None else n_rows.data_ptr(),
+                       None if row_starts is None else row_starts.data_ptr(),
+                       None if inv_freq is None else inv_freq.data_ptr(),
+                       None if err is None else err.data_ptr(), None, 0)
+        need = lib().orthrus_paged_append_workspace(ctypes.byref(a))
+        if need:
+            buf = _stream_ws(workspace, dev, "paged_append").get(need)
+            a.workspace, a.workspace_bytes = buf.data_ptr(), buf.numel()
+        _check("orthrus_paged_append", lib().orthrus_paged_append(ctypes.byref(a),
+                                                                  _stream(stream)))
+    return q_out
+
+
+def paged_block_attn(q, k_blk, v_blk, k_pages, v_pages, page_table, ctx_lens, mask_mode, *,
+                     shared_prefix=0, out=None, scale=None, max_ctx=None, err=None,
+                     workspace=None, stream=None):
+    """block_attn with the cache in pages (see orthrus_paged.h).
+
+    q [B, blk, Hq, D]; k_blk / v_blk [B, blk, Hkv, D], or both None when the
+    block's rows are in the pages already (ctx_lens then counts them); pools
+    [pages, Hkv, page_size, D]; page_table int32 [B, max_pages].
+    ``shared_prefix``: keys common to the whole batch, read once through row 0
+    of the table.  max_ctx bounds every ctx_lens entry (default: the table's
+    reach).  Returns out [B, blk, Hq, D]."""
+    _dev(q, k_blk, v_blk, k_pages, v_pages, page_table, ctx_lens, out, err)
+    if q.dim() != 4 or k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("q must be [B, blk, Hq, D], the pools [pages, Hkv, page_size, D], "
+                         "page_table [B, max_pages]")
+    B, blk, Hq, D = q.shape
+    pages, Hkv, page_size, _ = k_pages.shape
+    max_pages = page_table.shape[1]
+    dev = q.device
+    _like("k_pages", k_pages, q.dtype, dev, (pages, Hkv, page_size, D))
+    _like("v_pages", v_pages, q.dtype, dev, k_pages.shape)
+    if (k_blk is None) != (v_blk is None):
+        raise ValueError("k_blk and v_blk go together")
+    _like("k_blk", k_blk, q.dtype, dev, (B, blk, Hkv, D))
+    _like("v_blk", v_blk, q.dtype, dev, (B, blk, Hkv, D))
+    _like("page_table", page_table, torch.int32, dev, (B, max_pages))
+    _like("ctx_lens", ctx_lens, torch.int32, dev, (B,))
+    _like("out", out, q.dtype, dev, q.shape)
+    _like("err", err, torch.int32, dev)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        a = PagedAttnArgs(_dtype(q), int(mask_mode), B, Hq, Hkv, D, blk, page_size, pages,
+                          max_pages, max_pages * page_size if max_ctx is None else int(max_ctx),
+                          int(shared_prefix), float(D ** -0.5 if scale is None else scale), ptr(q),
+                          ptr(k_blk), ptr(v_blk), ptr(k_pages), ptr(v_pages), ptr(page_table),
+                          ptr(ctx_lens), ptr(out), ptr(err), None, 0)
+        need = lib().orthrus_paged_attn_workspace(ctypes.byref(a))
+        if need:
+            buf = _stream_ws(workspace, dev, "paged_attn").get(need)
+            a.workspace, a.workspace_bytes = buf.data_ptr(), buf.numel()
+        _check("orthrus_paged_attn", lib().orthrus_paged_attn(ctypes.byref(a), _stream(stream)))
+    return out
+
+
+def vocab_sample_filtered(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
+                          idx=None, logprob=None, err=None, stream=None):
+    """int32 [rows]: one token per row of softmax(logits / temperature) after
+    top-k, top-p and min-p, chosen by the row's uniform u (float32 [rows]; see
+    orthrus.h).  Each parameter is a number for all rows or a device tensor
+    [rows] (top_k int32, the others float32); None leaves it out.  ``logprob``
+    float32 [rows] receives the token's log-probability among those kept."""
+    if not logits.is_cuda or logits.dim() != 2 or (logits.numel() and logits.stride(1) != 1):
+        raise ValueError("logits must be a 2-D CUDA tensor with unit column stride")
+    rows, vocab = logits.shape
+    dev = logits.device
+
+    def per_row(name, v, dtype):
+        if v is None:
+            return None
+        if not torch.is_tensor(v):
+            return torch.full((rows,), v, dtype=dtype, device=dev)
+        _like(name, v, dtype, dev, (rows,))
+        return v
+
+    _like("u", u, torch.float32, dev, (rows,))
+    _like("idx", idx, torch.int32, dev, (rows,))
+    _like("logprob", logprob, torch.float32, dev, (rows,))
+    _like("err", err, torch.int32, dev)
+    _dev(u, idx, logprob, err)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    with _on(dev, stream):
+        temperature = per_row("temperature", temperature, torch.float32)
+        top_k = per_row("top_k", top_k, torch.int32)
+        top_p = per_row("top_p", top_p, torch.float32)
+        min_p = per_row("min_p", min_p, torch.float32)
+        _dev(temperature, top_k, top_p, min_p)
+        if idx is None:
+            idx = torch.empty(rows, dtype=torch.int32, device=dev)
+        a = FilterArgs(_dtype(logits), rows, vocab, max(logits.stride(0), vocab) if rows < 2
+                       else logits.stride(0), logits.data_ptr(), ptr(u), ptr(temperature),
+                       ptr(top_k), ptr(top_p), ptr(min_p), ptr(idx), ptr(logprob), ptr(err))
+        _check("orthrus_vocab_sample_filtered",
+               lib().orthrus_vocab_sample_filtered(ctypes.byref(a), _stream(stream)))
+    return idx

@@ -1,0 +1,419 @@
+// attn_paged_f32.cu -- FP32 block attention over a paged K/V cache on CUDA
+// cores, and the entry points of include/orthrus_paged.h's attention.
+//
+// Mathematics as in attn_paged.cu, in FP32 throughout (exp2f of scores scaled
+// by log2 e; running maximum and sum per row; partials of key ranges merged by
+// their maxima).
+//
+// CTA (split, kv-head, sequence): the G blk query rows, padded to R = 16 RPT,
+// against one range of keys in 64-key tiles.  256 threads form a 16 x 16 grid
+// over (row groups, column groups): a thread owns RPT rows, four keys of each
+// score tile and D/16 dims of the output, so a step of four dims costs
+// RPT + 4 shared-memory vectors for 16 RPT multiply-adds and the FP32 pipe, not
+// shared memory, bounds the tile products.  Q, K, V and P rows are padded by
+// four floats, which spreads the vectors of a column group over all banks.
+// K of the next tile loads (cp.async) while the softmax and the product with V
+// run, V of the next tile while its scores are taken.
+//
+// Row invariance.  Tiles and splits are cut by absolute key position, a
+// row's keys are taken in the same order whatever the block, and a masked key
+// adds an exact zero or nothing: with the same max_ctx, B and heads, a causal
+// row over (n cached keys, block) has the bits of a one-row call at its
+// position, as on orthrus_block_attn's FP32 path.
+//
+// Keys of the shared prefix are looked up through row 0 of the page table;
+// FP32 reads them once a sequence.
+#include <math.h>
+
+#include "attn_paged.cuh"
+#include "common.cuh"
+#include "tc_ptx.cuh"
+
+namespace orthrus {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 64;     // keys per tile
+constexpr int kMaxSplits = 256;
+
+struct F32Params {
+  const float *q, *k_blk, *v_blk, *k_pages, *v_pages;
+  const int32_t *ctx_lens, *table;
+  float* out;
+  int32_t* err;
+  float2* ml;  // [B][Hkv][S][rows] (m, l); m = NaN: a page was refused
+  float* o;    // [B][Hkv][S][rows][D]
+  int B, Hq, Hkv, G, blk, rows, page_size, pages, max_pages, max_ctx, P, causal, S, chunk;
+  float scale_log2;
+};
+
+template <int D, int RPT>
+constexpr int smem_floats() {
+  return 16 * RPT * (D + 4) + 2 * kKeys * (D + 4) + 16 * RPT * (kKeys + 4);
+}
+
+template <int D, int RPT>
+__global__ void __launch_bounds__(kThreads) f32_kernel(const F32Params p) {
+  constexpr int kLd = D + 4, kPLd = kKeys + 4, kDims = D / 16;  // dims of a thread
+  extern __shared__ float sm[];
+  float* Qs = sm;
+  float* Ks = Qs + 16 * RPT * kLd;
+  float* Vs = Ks + kKeys * kLd;
+  float* Ps = Vs + kKeys * kLd;
+  const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int n = p.ctx_lens[b];
+  if (n < 0 || n > p.max_ctx) {
+    if (split == 0 && g == 0 && tid == 0) set_err(p.err, ORTHRUS_ECAPACITY);
+    return;
+  }
+  const int total = n + (p.k_blk ? p.blk : 0);
+  const int lo = split * p.chunk, hi = min(total, lo + p.chunk);
+  const bool shared = p.P > 0 && n - (p.k_blk ? 0 : p.blk) >= p.P;
+  bool bad = false;
+
+  for (int e = tid; e < 16 * RPT * (D / 4); e += kThreads) {
+    const int r = e / (D / 4), c = e % (D / 4) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < p.rows)
+      v = load4(p.q + ((int64_t)(b * p.blk + r / p.G) * p.Hq + g * p.G + r % p.G) * D + c);
+    *reinterpret_cast<float4*>(Qs + r * kLd + c) = v;
+  }
+  // one 64-key tile of K or V; keys past the range are zero-filled
+  auto issue = [&](int k0, bool is_v) {
+    const float* pool = is_v ? p.v_pages : p.k_pages;
+    const float* blk = is_v ? p.v_blk : p.k_blk;
+    float* dst = is_v ? Vs : Ks;
+    for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
+      const int j = e / (D / 4), c = e % (D / 4) * 4;
+      const int pos = k0 + j;
+      const float* src = pool;
+      uint32_t bytes = 0;
+      if (pos < min(n, hi)) {
+        const int row = shared && pos < p.P ? 0 : b;
+        const int id = p.table[(int64_t)row * p.max_pages + pos / p.page_size];
+        if (id >= 0 && id < p.pages) {
+          src = pool + (((int64_t)id * p.Hkv + g) * p.page_size + pos % p.page_size) * D + c;
+          bytes = 16;
+        } else {
+          bad = true;
+        }
+      } else if (pos >= n && pos < hi) {
+        src = blk + ((int64_t)(b * p.blk + pos - n) * p.Hkv + g) * D + c;
+        bytes = 16;
+      }
+      ptx::cp_async16_zfill(ptx::smem_u32(dst + j * kLd + c), src, bytes);
+    }
+    ptx::cp_async_commit();
+  };
+
+  float o[RPT][kDims], m[RPT], l[RPT];
+  int lim[RPT];  // keys this row sees
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = ty * RPT + i;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    lim[i] = r >= p.rows ? 0 : p.causal ? total - p.blk + r / p.G + 1 : total;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) o[i][d] = 0.f;
+  }
+  const int zone = p.causal ? total - p.blk + 1 : total;  // from here on not every row sees
+  if (lo < hi) {
+    issue(lo, false);
+    issue(lo, true);
+  }
+  for (int k0 = lo; k0 < hi; k0 += kKeys) {
+    ptx::cp_async_wait<1>();  // K(k0), or everything older than the last group
+    __syncthreads();
+    // ---- scores: rows ty*RPT.., keys tx + 16 j (a column group's key rows
+    // lie 16 apart, so that their vectors fall into different banks)
+    float s[RPT][4];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+      float4 kf[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        kf[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * kLd + d);
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const float4 qf = *reinterpret_cast<const float4*>(Qs + (ty * RPT + i) * kLd + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(qf.x, kf[j].x, s[i][j]);
+          s[i][j] = fmaf(qf.y, kf[j].y, s[i][j]);
+          s[i][j] = fmaf(qf.z, kf[j].z, s[i][j]);
+          s[i][j] = fmaf(qf.w, kf[j].w, s[i][j]);
+        }
+      }
+    }
+    __syncthreads();  // K is read
+    const bool more = k0 + kKeys < hi;
+    if (more) issue(k0 + kKeys, false);
+    // ---- softmax of the tile, row by row over the 16 threads of a row group
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      float mt = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = k0 + tx + 16 * j;
+        s[i][j] = key < min(lim[i], hi) ? __fmul_rn(s[i][j], p.scale_log2) : -INFINITY;
+        mt = fmaxf(mt, s[i][j]);
+      }
+#pragma unroll
+      for (int w = 8; w; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));
+      const float mn = fmaxf(m[i], mt);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float f = m[i] == mn ? 1.f : exp2f(m[i] - mn);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = exp2f(__fsub_rn(s[i][j], base));
+        sum += s[i][j];
+        Ps[(ty * RPT + i) * kPLd + tx + 16 * j] = s[i][j];
+      }
+#pragma unroll
+      for (int w = 8; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      l[i] = fmaf(l[i], f, sum);
+      m[i] = mn;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) o[i][d] *= f;
+    }
+    if (more) ptx::cp_async_wait<1>(); else ptx::cp_async_wait<0>();  // V(k0)
+    __syncthreads();
+    // ---- O += P V: dims 4 tx + 64 d + (0..3)
+    const int keys = min(kKeys, hi - k0);
+    if (k0 + keys <= zone) {
+#pragma unroll 2
+      for (int j = 0; j < kKeys; j += 4) {
+        float4 pf[RPT];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+          pf[i] = *reinterpret_cast<const float4*>(Ps + (ty * RPT + i) * kPLd + j);
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+#pragma unroll
+          for (int d = 0; d < kDims / 4; ++d) {
+            const float4 vf =
+                *reinterpret_cast<const float4*>(Vs + (j + jj) * kLd + 4 * tx + 64 * d);
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+              const float w = jj == 0 ? pf[i].x : jj == 1 ? pf[i].y : jj == 2 ? pf[i].z : pf[i].w;
+              o[i][4 * d] = fmaf(w, vf.x, o[i][4 * d]);
+              o[i][4 * d + 1] = fmaf(w, vf.y, o[i][4 * d + 1]);
+              o[i][4 * d + 2] = fmaf(w, vf.z, o[i][4 * d + 2]);
+              o[i][4 * d + 3] = fmaf(w, vf.w, o[i][4 * d + 3]);
+            }
+          }
+        }
+      }
+    } else {
+      // some rows do not see some keys: their V may be NaN or infinite there
+      for (int j = 0; j < keys; ++j) {
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+          if (k0 + j >= lim[i]) continue;
+          const float w = Ps[(ty * RPT + i) * kPLd + j];
+#pragma unroll
+          for (int d = 0; d < kDims; ++d)
+            o[i][d] = fmaf(w, Vs[j * kLd + 4 * tx + 64 * (d / 4) + d % 4], o[i][d]);
+        }
+      }
+    }
+    __syncthreads();  // V and P are read
+    if (more) issue(k0 + kKeys, true);
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) set_err(p.err, ORTHRUS_EINVAL);
+  const int64_t at = ((int64_t)(b * p.Hkv + g) * p.S + split) * p.rows;
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = ty * RPT + i;
+    if (r >= p.rows) continue;
+    if (p.S == 1) {
+      if (bad) continue;
+      float* out = p.out + ((int64_t)(b * p.blk + r / p.G) * p.Hq + g * p.G + r % p.G) * D;
+      const float inv = 1.f / l[i];
+#pragma unroll
+      for (int d = 0; d < kDims; ++d)
+        out[4 * tx + 64 * (d / 4) + d % 4] = lim[i] > 0 ? o[i][d] * inv : 0.f;
+      continue;
+    }
+#pragma unroll
+    for (int d = 0; d < kDims / 4; ++d)
+      *reinterpret_cast<float4*>(p.o + (at + r) * D + 4 * tx + 64 * d) =
+          make_float4(o[i][4 * d], o[i][4 * d + 1], o[i][4 * d + 2], o[i][4 * d + 3]);
+    if (tx == 0) p.ml[at + r] = make_float2(bad ? __int_as_float(0x7fffffff) : m[i], l[i]);
+  }
+}
+
+// One warp per query row, D/32 dims a lane; splits in index order.
+template <int D>
+__global__ void __launch_bounds__(128) f32_merge(const F32Params p) {
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= p.B * p.Hkv * p.rows) return;
+  const int r = row % p.rows, bg = row / p.rows, b = bg / p.Hkv, g = bg % p.Hkv;
+  const int n = p.ctx_lens[b];
+  if (n < 0 || n > p.max_ctx) return;
+  const int total = n + (p.k_blk ? p.blk : 0);
+  const int S = ceil_div(total, p.chunk);  // splits that hold keys
+  const int64_t at = (int64_t)bg * p.S * p.rows + r;
+  float M = -INFINITY, L = 0.f, acc[D / 32];
+  bool bad = false;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) acc[d] = 0.f;
+  for (int s = 0; s < S; ++s) {
+    const float2 ml = p.ml[at + (int64_t)s * p.rows];
+    if (ml.x != ml.x) bad = true;
+    if (ml.y == 0.f) continue;  // the row sees no key of this split
+    const float m = fmaxf(M, ml.x);
+    const float wa = M == m ? 1.f : exp2f(M - m), wb = ml.x == m ? 1.f : exp2f(ml.x - m);
+    L = fmaf(wa, L, __fmul_rn(wb, ml.y));
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+      acc[d] = fmaf(wa, acc[d], __fmul_rn(wb, p.o[(at + (int64_t)s * p.rows) * D + lane + 32 * d]));
+    M = m;
+  }
+  if (bad) return;
+  const int i = r / p.G;
+  const int lim = p.causal ? total - p.blk + i + 1 : total;
+  float* out = p.out + ((int64_t)(b * p.blk + i) * p.Hq + g * p.G + r % p.G) * D;
+  const float inv = 1.f / L;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) out[lane + 32 * d] = lim > 0 ? acc[d] * inv : 0.f;
+}
+
+// Keys per CTA: whole tiles, about two CTAs for every SM of a B200.  The same
+// for every block size (32 stands for blk), see the note on row invariance.
+int plan_chunk(const orthrus_paged_attn_args& a) {
+  const int tiles = ceil_div(a.max_ctx + 32, kKeys);
+  int S = ceil_div(2 * 148, max(1, a.B * a.Hkv));
+  S = min(min(S, tiles), kMaxSplits);
+  return ceil_div(tiles, S) * kKeys;
+}
+
+int plan_splits(const orthrus_paged_attn_args& a, int chunk) {
+  return max(1, ceil_div(a.max_ctx + a.blk, chunk));
+}
+
+template <int D, int RPT>
+cudaError_t launch(const F32Params& p, cudaStream_t st) {
+  constexpr int smem = smem_floats<D, RPT>() * 4;
+  static bool done[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(f32_kernel<D, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev] = true;
+  }
+  f32_kernel<D, RPT><<<dim3(p.S, p.Hkv, p.B), kThreads, smem, st>>>(p);
+  if (p.S > 1) f32_merge<D><<<ceil_div(p.B * p.Hkv * p.rows, 4), 128, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_rows(const F32Params& p, cudaStream_t st) {
+  if (p.rows <= 16) return launch<D, 1>(p, st);
+  if (p.rows <= 32) return launch<D, 2>(p, st);
+  if (p.rows <= 64) return launch<D, 4>(p, st);
+  return launch<D, 8>(p, st);
+}
+
+int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+int check_shape(const orthrus_paged_attn_args* a) {
+  if (!a) return ORTHRUS_EINVAL;
+  if (a->dtype != ORTHRUS_F32 && a->dtype != ORTHRUS_BF16) return ORTHRUS_EINVAL;
+  if (a->mask_mode != ORTHRUS_BIDIR_BLOCK && a->mask_mode != ORTHRUS_CAUSAL_VERIFY)
+    return ORTHRUS_EINVAL;
+  if (a->B < 0 || a->Hq <= 0 || a->Hkv <= 0 || a->D <= 0 || a->blk <= 0 || a->page_size <= 0 ||
+      a->pages <= 0 || a->max_pages <= 0 || a->max_ctx < 0 || a->shared_prefix < 0)
+    return ORTHRUS_EINVAL;
+  if (a->Hq % a->Hkv) return ORTHRUS_EINVAL;
+  if (!isfinite(a->scale) || !(a->scale > 0.f)) return ORTHRUS_EINVAL;
+  if (a->max_ctx > (int64_t)a->max_pages * a->page_size) return ORTHRUS_ECAPACITY;
+  if (a->shared_prefix > a->max_ctx) return ORTHRUS_EINVAL;
+  if (a->D != 64 && a->D != 128) return ORTHRUS_EUNSUPPORTED;
+  if (a->blk > 32 || (int64_t)(a->Hq / a->Hkv) * a->blk > 128) return ORTHRUS_EUNSUPPORTED;
+  if (a->page_size < 16 || a->page_size > 256 || (a->page_size & (a->page_size - 1)))
+    return ORTHRUS_EUNSUPPORTED;
+  if ((a->k_blk != nullptr) != (a->v_blk != nullptr)) return ORTHRUS_EINVAL;
+  // grid limits, and 32-bit tile, row and slot numbers
+  const int64_t tiles = a->max_ctx / 64 + 2;
+  if (a->B > 65535 || a->Hkv > 65535 || (int64_t)a->B * a->Hkv * tiles > (1 << 30) ||
+      (int64_t)a->B * a->blk * a->Hq > (1 << 30) ||
+      (int64_t)a->pages * a->Hkv * a->page_size > 0x7fffffffll)
+    return ORTHRUS_EUNSUPPORTED;
+  return ORTHRUS_OK;
+}
+
+}  // namespace
+
+size_t paged_f32_workspace(const orthrus_paged_attn_args& a) {
+  const int S = plan_splits(a, plan_chunk(a));
+  if (S == 1) return 0;
+  const int64_t parts = (int64_t)a.B * a.Hq * a.blk * S;
+  return (size_t)(up256(parts * 8) + up256(parts * a.D * 4));
+}
+
+int paged_f32_launch(const orthrus_paged_attn_args& a, cudaStream_t st) {
+  F32Params p;
+  p.q = static_cast<const float*>(a.q);
+  p.k_blk = static_cast<const float*>(a.k_blk);
+  p.v_blk = static_cast<const float*>(a.v_blk);
+  p.k_pages = static_cast<const float*>(a.k_pages);
+  p.v_pages = static_cast<const float*>(a.v_pages);
+  p.ctx_lens = a.ctx_lens; p.table = a.page_table;
+  p.out = static_cast<float*>(a.out);
+  p.err = a.err;
+  p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.blk = a.blk;
+  p.rows = p.G * a.blk; p.page_size = a.page_size; p.pages = a.pages;
+  p.max_pages = a.max_pages; p.max_ctx = a.max_ctx; p.P = a.shared_prefix;
+  p.causal = a.mask_mode == ORTHRUS_CAUSAL_VERIFY;
+  p.chunk = plan_chunk(a);
+  p.S = plan_splits(a, p.chunk);
+  p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+  const int64_t parts = (int64_t)a.B * a.Hq * a.blk * p.S;
+  p.ml = static_cast<float2*>(a.workspace);
+  p.o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + up256(parts * 8));
+  const cudaError_t e = a.D == 64 ? launch_rows<64>(p, st) : launch_rows<128>(p, st);
+  return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ECUDA;
+}
+
+}  // namespace orthrus
+
+using namespace orthrus;
+
+extern "C" {
+
+size_t orthrus_paged_attn_workspace(const orthrus_paged_attn_args* a) {
+  if (check_shape(a) != ORTHRUS_OK || a->B == 0) return 0;
+  return a->dtype == ORTHRUS_BF16 ? paged_tc_workspace(*a) : paged_f32_workspace(*a);
+}
+
+int orthrus_paged_attn(const orthrus_paged_attn_args* a, orthrus_stream_t stream) {
+  const int rc = check_shape(a);
+  if (rc != ORTHRUS_OK) return rc;
+  if (a->B == 0) return ORTHRUS_OK;
+  const void* ptrs[] = {a->q, a->k_pages, a->v_pages, a->out};
+  for (const void* p : ptrs)
+    if (!p || !aligned(p, 16)) return ORTHRUS_EINVAL;
+  if (!aligned(a->k_blk, 16) || !aligned(a->v_blk, 16)) return ORTHRUS_EINVAL;
+  if (!a->page_table || !a->ctx_lens) return ORTHRUS_EINVAL;
+  const size_t need = orthrus_paged_attn_workspace(a);
+  if (need > 0 && (!a->workspace || a->workspace_bytes < need || !aligned(a->workspace, 256)))
+    return ORTHRUS_EWORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return a->dtype == ORTHRUS_BF16 ? paged_tc_launch(*a, st) : paged_f32_launch(*a, st);
+}
+
+}  // extern "C"

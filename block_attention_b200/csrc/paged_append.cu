@@ -1,0 +1,451 @@
+// paged_append.cu -- rotary positions and the rows of a paged K/V cache
+// (include/orthrus_paged.h).
+//
+// One kernel serves both entry points.  A CTA takes R consecutive rows: its
+// threads first evaluate the rows' scaled cosines and sines once for all
+// heads (FP64 angle in half turns, sincospi, rounded to FP32, in shared
+// memory) and look up each row's page, then walk the (row, head, chunk) units
+// of q, k and v.  A unit is one 16-byte chunk (two, a pair of halves, in the
+// half layout), so every element is read and written once with full sectors:
+// the path is bound by HBM for a prefill and by launch latency for a decoding
+// step.  When strides, alignment or rot do not allow 16-byte chunks the same
+// walk runs element by element.
+#include <math.h>
+
+#include "common.cuh"
+#include "orthrus_paged.h"
+
+namespace orthrus {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRows = 16;  // rows per CTA at most (shared row records)
+constexpr int kMaxHeadDim = 1024;
+constexpr int kTableBytes = 16384;  // cosine / sine pairs a CTA may hold
+
+struct RowParams {
+  // the three row tensors: q (rotated to q_out), k (rotated into pages), v
+  const void *q, *k, *v;
+  int64_t q_row, q_head, k_layer, k_row, k_head, v_layer, v_row, v_head;
+  void* q_out;
+  int64_t qo_row, qo_head;
+  void *k_pages, *v_pages;
+  int64_t pages_layer;
+  const int32_t *page_table, *n_rows, *row_starts, *positions;
+  int32_t* ctx_lens;
+  const double* inv_freq;
+  int32_t* err;
+  unsigned* ticket;
+  int B, blk, rows, Hq, Hkv, D, page_size, pages, max_pages, rot, R, advance;
+  double mscale, sign;
+};
+
+// Sequence of row r in the ragged form: the last b with row_starts[b] <= r
+// (empty sequences share a start with their successor, which wins).
+__device__ __forceinline__ int find_seq(const int32_t* starts, int B, int r) {
+  int lo = 0, hi = B;  // starts[lo] <= r < starts[hi] is kept
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] <= r) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Rows that sequence b appends; -1 if its counts or length are out of range.
+__device__ __forceinline__ int taken_rows(const RowParams& p, int b, int n) {
+  int cnt = p.blk;
+  if (p.row_starts) cnt = p.row_starts[b + 1] - p.row_starts[b];
+  else if (p.n_rows) cnt = p.n_rows[b];
+  if (n < 0 || cnt < 0 || (!p.row_starts && cnt > p.blk)) return -1;
+  return cnt;
+}
+
+struct Row {
+  int64_t pos;   // rotation angle's position
+  int64_t base;  // element offset of (page, head 0, slot) in a pool, < 0: not written
+  int q_ok;      // the row is taken: its queries are rotated
+};
+
+__device__ __forceinline__ Row locate(const RowParams& p, int r, bool first) {
+  Row o{0, -1, 0};
+  if (p.positions) {
+    o.pos = p.positions[r];
+    o.q_ok = 1;
+    return o;
+  }
+  int b, j;
+  if (p.row_starts) {
+    if (r < p.row_starts[0] || r >= p.row_starts[p.B]) return o;
+    b = find_seq(p.row_starts, p.B, r);
+    j = r - p.row_starts[b];
+  } else {
+    b = r / p.blk;
+    j = r - b * p.blk;
+  }
+  const int n = p.ctx_lens[b];
+  const int cnt = taken_rows(p, b, n);
+  if (cnt < 0 && first) set_err(p.err, ORTHRUS_ECAPACITY);
+  if (j >= cnt) return o;
+  o.pos = (int64_t)n + j;
+  o.q_ok = 1;
+  const int64_t pg = o.pos / p.page_size;
+  if (pg >= p.max_pages) {
+    if (first) set_err(p.err, ORTHRUS_ECAPACITY);
+    return o;
+  }
+  const int id = p.page_table[(int64_t)b * p.max_pages + pg];
+  if (id < 0 || id >= p.pages) {
+    if (first) set_err(p.err, ORTHRUS_EINVAL);
+    return o;
+  }
+  const int slot = (int)(o.pos - pg * p.page_size);
+  o.base = ((int64_t)id * p.Hkv * p.page_size + slot) * p.D;
+  return o;
+}
+
+// One 16-byte chunk (kV elements) or one element (kV == 1) as floats.
+template <typename T, int kV>
+__device__ __forceinline__ void load_v(const T* p, float (&v)[kV]) {
+  if constexpr (kV == 1) {
+    v[0] = to_f32(p[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  } else {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+template <typename T, int kV>
+__device__ __forceinline__ void store_v(T* p, const float (&v)[kV]) {
+  if constexpr (kV == 1) {
+    p[0] = from_f32<T>(v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(h);
+  }
+}
+
+// Rotate or copy unit c of one head.  Units of a rotated head: rot/2 pairs in
+// groups of kV (half layout: chunk c and its partner rot/2 further on;
+// interleaved: one chunk holds kV/2 pairs, or for kV == 1 one pair), then the
+// D - rot values that pass through, in groups of kV.
+template <typename T, int kV, bool kInter>
+__device__ __forceinline__ void turn_unit(const T* src, T* dst, int c, int turn_units, int rot,
+                                          const float2* cs) {
+  if (c >= turn_units) {
+    const int e = rot + (c - turn_units) * kV;
+    float v[kV];
+    load_v<T, kV>(src + e, v);
+    store_v<T, kV>(dst + e, v);
+    return;
+  }
+  if constexpr (kInter && kV > 1) {
+    float v[kV], w[kV];
+    load_v<T, kV>(src + c * kV, v);
+#pragma unroll
+    for (int i = 0; i < kV / 2; ++i) {
+      const float2 t = cs[c * (kV / 2) + i];
+      w[2 * i] = rope_first(v[2 * i], v[2 * i + 1], t);
+      w[2 * i + 1] = rope_second(v[2 * i], v[2 * i + 1], t);
+    }
+    store_v<T, kV>(dst + c * kV, w);
+  } else {
+    const int a = kInter ? 2 * c : c * kV;
+    const int b = kInter ? 2 * c + 1 : c * kV + rot / 2;
+    float x1[kV], x2[kV], y1[kV], y2[kV];
+    load_v<T, kV>(src + a, x1);
+    load_v<T, kV>(src + b, x2);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const float2 t = cs[c * kV + i];
+      y1[i] = rope_first(x1[i], x2[i], t);
+      y2[i] = rope_second(x1[i], x2[i], t);
+    }
+    store_v<T, kV>(dst + a, y1);
+    store_v<T, kV>(dst + b, y2);
+  }
+}
+
+template <typename T, int kV, bool kInter>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const RowParams p) {
+  extern __shared__ float2 cs[];  // [R][rot/2] scaled (cos, sin)
+  __shared__ Row row[kMaxRows];
+  const int layer = blockIdx.y;
+  const int r0 = blockIdx.x * p.R;
+  const int nr = min(p.R, p.rows - r0);
+  const int half = p.rot / 2;
+  if (threadIdx.x < nr) row[threadIdx.x] = locate(p, r0 + threadIdx.x, layer == 0);
+  __syncthreads();
+  for (int e = threadIdx.x; e < nr * half; e += kThreads) {
+    const int rr = e / half, i = e - rr * half;
+    // angle in half turns: the reduction to one turn is exact in sincospi
+    double sn, cn;
+    sincospi((double)row[rr].pos * p.inv_freq[i] * 0.31830988618379067154, &sn, &cn);
+    cs[e] = make_float2((float)(p.mscale * cn), (float)(p.sign * p.mscale * sn));
+  }
+  __syncthreads();
+
+  const int turn_units = kInter && kV > 1 ? p.rot / kV : half / kV;
+  const int head_units = turn_units + (p.D - p.rot) / kV;  // of a rotated head
+  const int copy_units = p.D / kV;                         // of a V head
+  const int qk = (p.Hq + p.Hkv) * head_units;
+  const int per_row = qk + p.Hkv * copy_units;
+  for (int e = threadIdx.x; e < nr * per_row; e += kThreads) {
+    const int rr = e / per_row;
+    int u = e - rr * per_row;
+    const Row& rw = row[rr];
+    const int64_t r = r0 + rr;
+    if (u < qk) {
+      const int h = u / head_units, c = u - h * head_units;
+      const T* src;
+      T* dst;
+      if (h < p.Hq) {
+        if (!rw.q_ok) continue;
+        src = static_cast<const T*>(p.q) + r * p.q_row + h * p.q_head;
+        dst = static_cast<T*>(p.q_out) + r * p.qo_row + h * p.qo_head;
+      } else {
+        if (rw.base < 0) continue;
+        const int g = h - p.Hq;
+        src = static_cast<const T*>(p.k) + layer * p.k_layer + r * p.k_row + g * p.k_head;
+        dst = static_cast<T*>(p.k_pages) + layer * p.pages_layer + rw.base +
+              (int64_t)g * p.page_size * p.D;
+      }
+      turn_unit<T, kV, kInter>(src, dst, c, turn_units, p.rot, cs + rr * half);
+    } else {
+      if (rw.base < 0) continue;
+      u -= qk;
+      const int g = u / copy_units, c = u - g * copy_units;
+      float v[kV];
+      load_v<T, kV>(static_cast<const T*>(p.v) + layer * p.v_layer + r * p.v_row +
+                        g * p.v_head + c * kV, v);
+      store_v<T, kV>(static_cast<T*>(p.v_pages) + layer * p.pages_layer + rw.base +
+                         (int64_t)g * p.page_size * p.D + c * kV, v);
+    }
+  }
+
+  if (!p.advance) return;
+  // the last CTA (every other has read the lengths) advances them
+  __shared__ int last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const unsigned total = gridDim.x * gridDim.y;
+    last = atomicAdd(p.ticket, 1u) == total - 1u;
+    if (last) *p.ticket = 0u;
+  }
+  __syncthreads();
+  if (!last) return;
+  for (int b = threadIdx.x >> 5; b < p.B; b += kThreads / 32) {
+    const int n = p.ctx_lens[b];
+    const int cnt = taken_rows(p, b, n);
+    bool ok = cnt > 0 && ((int64_t)n + cnt - 1) / p.page_size < p.max_pages;
+    if (ok)
+      for (int64_t pg = n / p.page_size + (threadIdx.x & 31);
+           pg <= ((int64_t)n + cnt - 1) / p.page_size; pg += 32) {
+        const int id = p.page_table[(int64_t)b * p.max_pages + pg];
+        ok = ok && id >= 0 && id < p.pages;
+      }
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok && (threadIdx.x & 31) == 0) p.ctx_lens[b] = n + cnt;
+  }
+}
+
+template <typename T, int kV>
+cudaError_t launch_rows(const RowParams& p, int layout, int layers, cudaStream_t st) {
+  const dim3 grid(ceil_div(p.rows, p.R), layers);
+  const size_t smem = (size_t)p.R * (p.rot / 2) * sizeof(float2);
+  if (layout == ORTHRUS_ROPE_INTERLEAVED)
+    rows_kernel<T, kV, true><<<grid, kThreads, smem, st>>>(p);
+  else
+    rows_kernel<T, kV, false><<<grid, kThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+bool dtype_ok(int32_t t) { return t == ORTHRUS_F32 || t == ORTHRUS_BF16; }
+bool multiple(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int status(cudaError_t e) { return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ECUDA; }
+
+// Rows per CTA: enough units for its threads, few enough that the rows still
+// spread over the SMs, within the shared table.
+int rows_per_cta(const RowParams& p, int vec) {
+  const int64_t units = (int64_t)(p.Hq + 2 * p.Hkv) * p.D / vec;
+  int R = (int)(4 * kThreads / (units > 0 ? units : 1));
+  const int spread = ceil_div(p.rows, 148);
+  if (R > spread) R = spread;
+  const int table = kTableBytes / (int)((p.rot / 2 > 0 ? p.rot / 2 : 1) * sizeof(float2));
+  if (R > table) R = table;
+  if (R > kMaxRows) R = kMaxRows;
+  return R < 1 ? 1 : R;
+}
+
+int run_rows(RowParams& p, int dtype, int layout, int layers, bool vec_ok, cudaStream_t st) {
+  const int es = dtype == ORTHRUS_F32 ? 4 : 2, w = 16 / es;
+  // whole 16-byte chunks on both halves of every head
+  const int grain = layout == ORTHRUS_ROPE_INTERLEAVED ? p.rot : p.rot / 2;
+  const bool vec = vec_ok && grain % w == 0 && (p.D - p.rot) % w == 0 && p.D % w == 0;
+  p.R = rows_per_cta(p, vec ? w : 1);
+  if (dtype == ORTHRUS_F32)
+    return status(vec ? launch_rows<float, 4>(p, layout, layers, st)
+                      : launch_rows<float, 1>(p, layout, layers, st));
+  return status(vec ? launch_rows<__nv_bfloat16, 8>(p, layout, layers, st)
+                    : launch_rows<__nv_bfloat16, 1>(p, layout, layers, st));
+}
+
+int check_rope(int dtype, int layout, int rows, int D, int rot, double mscale,
+               const double* inv_freq) {
+  if (!dtype_ok(dtype)) return ORTHRUS_EINVAL;
+  if (layout != ORTHRUS_ROPE_HALF && layout != ORTHRUS_ROPE_INTERLEAVED) return ORTHRUS_EINVAL;
+  if (rows < 0 || D < 1 || rot < 0 || rot > D || rot % 2) return ORTHRUS_EINVAL;
+  if (D > kMaxHeadDim) return ORTHRUS_EUNSUPPORTED;
+  if (!isfinite(mscale)) return ORTHRUS_EINVAL;
+  if (rot > 0 && (!inv_freq || !multiple(inv_freq, 8))) return ORTHRUS_EINVAL;
+  return ORTHRUS_OK;
+}
+
+}  // namespace
+}  // namespace orthrus
+
+using namespace orthrus;
+
+extern "C" {
+
+int orthrus_rope_freqs(int32_t rot, double theta, const orthrus_rope_scaling* s,
+                       double* inv_freq, double* mscale) {
+  if (rot < 2 || rot % 2 || !isfinite(theta) || !(theta > 1.0) || !inv_freq || !mscale)
+    return ORTHRUS_EINVAL;
+  const int kind = s ? s->kind : ORTHRUS_ROPE_PLAIN;
+  if (kind < ORTHRUS_ROPE_PLAIN || kind > ORTHRUS_ROPE_YARN) return ORTHRUS_EINVAL;
+  const double two_pi = 6.283185307179586477;
+  double base = theta;
+  if (kind != ORTHRUS_ROPE_PLAIN && (!isfinite(s->factor) || !(s->factor >= 1.0)))
+    return ORTHRUS_EINVAL;
+  if (kind == ORTHRUS_ROPE_NTK) {
+    if (rot < 4) return ORTHRUS_EINVAL;
+    base = theta * pow(s->factor, (double)rot / (rot - 2));
+  }
+  double lo = 0, hi = 0;
+  if (kind == ORTHRUS_ROPE_BANDS || kind == ORTHRUS_ROPE_YARN) {
+    if (!isfinite(s->original_ctx) || !(s->original_ctx > 0) || !(s->low > 0) ||
+        !isfinite(s->high) || !(s->high > s->low))
+      return ORTHRUS_EINVAL;
+    if (kind == ORTHRUS_ROPE_YARN) {
+      if (!isfinite(s->mscale) || s->mscale < 0) return ORTHRUS_EINVAL;
+      // index whose frequency makes n turns over the trained context
+      const double k = rot / (2 * log(theta));
+      lo = fmax(floor(k * log(s->original_ctx / (two_pi * s->high))), 0.0);
+      hi = fmin(ceil(k * log(s->original_ctx / (two_pi * s->low))), rot - 1.0);
+    }
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot);
+    if (kind == ORTHRUS_ROPE_LINEAR) {
+      f /= s->factor;
+    } else if (kind == ORTHRUS_ROPE_BANDS) {
+      const double turns = s->original_ctx * f / two_pi;
+      const double t = fmin(fmax((turns - s->low) / (s->high - s->low), 0.0), 1.0);
+      f = (1 - t) * f / s->factor + t * f;
+    } else if (kind == ORTHRUS_ROPE_YARN) {
+      const double t = fmin(fmax((i - lo) / fmax(hi - lo, 1e-3), 0.0), 1.0);
+      f = (1 - t) * f + t * f / s->factor;
+    }
+    inv_freq[i] = f;
+  }
+  *mscale = 1.0;
+  if (kind == ORTHRUS_ROPE_YARN) *mscale = s->mscale > 0 ? s->mscale : 0.1 * log(s->factor) + 1;
+  return ORTHRUS_OK;
+}
+
+int orthrus_rope(const orthrus_rope_args* a, orthrus_stream_t stream) {
+  if (!a) return ORTHRUS_EINVAL;
+  const int rc = check_rope(a->dtype, a->layout, a->rows, a->D, a->rot, a->mscale, a->inv_freq);
+  if (rc != ORTHRUS_OK) return rc;
+  if (a->H < 1 || a->inverse < 0 || a->inverse > 1 || a->x_row_stride < 0 ||
+      a->x_head_stride < 0 || a->out_row_stride < 0 || a->out_head_stride < 0)
+    return ORTHRUS_EINVAL;
+  if ((int64_t)a->H * a->D > (1 << 24)) return ORTHRUS_EUNSUPPORTED;
+  if (a->rows == 0) return ORTHRUS_OK;
+  const int es = a->dtype == ORTHRUS_F32 ? 4 : 2;
+  if (!a->x || !a->out || !a->positions || !multiple(a->x, es) || !multiple(a->out, es))
+    return ORTHRUS_EINVAL;
+  if (a->x == a->out && (a->x_row_stride != a->out_row_stride ||
+                         a->x_head_stride != a->out_head_stride))
+    return ORTHRUS_EINVAL;
+  RowParams p = {};
+  p.q = a->x; p.q_row = a->x_row_stride; p.q_head = a->x_head_stride;
+  p.q_out = a->out; p.qo_row = a->out_row_stride; p.qo_head = a->out_head_stride;
+  p.positions = a->positions; p.inv_freq = a->inv_freq;
+  p.rows = a->rows; p.Hq = a->H; p.D = a->D; p.rot = a->rot; p.page_size = 1;
+  p.mscale = a->mscale; p.sign = a->inverse ? -1.0 : 1.0;
+  const int w = 16 / es;
+  const bool vec = multiple(a->x, 16) && multiple(a->out, 16) && a->x_row_stride % w == 0 &&
+                   a->x_head_stride % w == 0 && a->out_row_stride % w == 0 &&
+                   a->out_head_stride % w == 0;
+  return run_rows(p, a->dtype, a->layout, 1, vec, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t orthrus_paged_append_workspace(const orthrus_append_args* a) {
+  return a && a->advance ? 256 : 0;
+}
+
+int orthrus_paged_append(const orthrus_append_args* a, orthrus_stream_t stream) {
+  if (!a) return ORTHRUS_EINVAL;
+  const int rc = check_rope(a->dtype, a->layout, a->rows, a->D, a->rot, a->mscale, a->inv_freq);
+  if (rc != ORTHRUS_OK) return rc;
+  if (a->layers < 1 || a->B < 0 || a->blk < 0 || a->Hkv < 1 || a->Hq < 0 || a->page_size < 1 ||
+      a->pages < 1 || a->max_pages < 1 || a->advance < 0 || a->advance > 1)
+    return ORTHRUS_EINVAL;
+  if (a->layers > 65535 || (int64_t)(a->Hq + 2ll * a->Hkv) * a->D > (1 << 24))
+    return ORTHRUS_EUNSUPPORTED;
+  if ((a->q != nullptr) != (a->Hq > 0) || (a->q && a->layers != 1)) return ORTHRUS_EINVAL;
+  if (a->row_starts ? a->n_rows != nullptr : (int64_t)a->B * a->blk != a->rows)
+    return ORTHRUS_EINVAL;
+  const int64_t strides[] = {a->k_layer_stride, a->k_row_stride, a->k_head_stride,
+                             a->v_layer_stride, a->v_row_stride, a->v_head_stride,
+                             a->q_row_stride,   a->q_head_stride, a->pages_layer_stride};
+  for (int64_t s : strides)
+    if (s < 0) return ORTHRUS_EINVAL;
+  const int64_t pool = (int64_t)a->pages * a->Hkv * a->page_size * a->D;
+  if (a->layers > 1 && a->pages_layer_stride < pool) return ORTHRUS_EINVAL;
+  if (a->B == 0 || a->rows == 0) return ORTHRUS_OK;
+  const int es = a->dtype == ORTHRUS_F32 ? 4 : 2;
+  const void* ptrs[] = {a->k, a->v, a->k_pages, a->v_pages};
+  for (const void* q : ptrs)
+    if (!q || !multiple(q, es)) return ORTHRUS_EINVAL;
+  if (a->q && (!a->q_out || !multiple(a->q, es) || !multiple(a->q_out, es))) return ORTHRUS_EINVAL;
+  if (!a->page_table || !a->ctx_lens) return ORTHRUS_EINVAL;
+  if (a->advance && (!a->workspace || a->workspace_bytes < orthrus_paged_append_workspace(a) ||
+                     !multiple(a->workspace, 4)))
+    return ORTHRUS_EWORKSPACE;
+  RowParams p = {};
+  p.q = a->q; p.k = a->k; p.v = a->v;
+  p.q_row = a->q_row_stride; p.q_head = a->q_head_stride;
+  p.k_layer = a->k_layer_stride; p.k_row = a->k_row_stride; p.k_head = a->k_head_stride;
+  p.v_layer = a->v_layer_stride; p.v_row = a->v_row_stride; p.v_head = a->v_head_stride;
+  p.q_out = a->q_out; p.qo_row = (int64_t)a->Hq * a->D; p.qo_head = a->D;
+  p.k_pages = a->k_pages; p.v_pages = a->v_pages; p.pages_layer = a->pages_layer_stride;
+  p.page_table = a->page_table; p.n_rows = a->n_rows; p.row_starts = a->row_starts;
+  p.ctx_lens = a->ctx_lens; p.inv_freq = a->inv_freq; p.err = a->err;
+  p.ticket = static_cast<unsigned*>(a->workspace);
+  p.B = a->B; p.blk = a->blk; p.rows = a->rows; p.Hq = a->Hq; p.Hkv = a->Hkv; p.D = a->D;
+  p.page_size = a->page_size; p.pages = a->pages; p.max_pages = a->max_pages;
+  p.rot = a->rot; p.advance = a->advance; p.mscale = a->mscale; p.sign = 1.0;
+  const int w = 16 / es;
+  bool vec = a->pages_layer_stride % w == 0;
+  for (const void* q : ptrs) vec = vec && multiple(q, 16);
+  if (a->q) vec = vec && multiple(a->q, 16) && multiple(a->q_out, 16);
+  for (int64_t s : strides) vec = vec && s % w == 0;
+  return run_rows(p, a->dtype, a->layout, a->layers, vec, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

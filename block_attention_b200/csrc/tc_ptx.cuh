@@ -360,6 +360,14 @@ __device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, uint32_t
       ::"r"(dst_cluster), "r"(src_cta), "r"(bytes), "r"(bar_cluster)
       : "memory");
 }
+// Give registers back to, or take them from, the pool the CTA was launched
+// with; every warp of the warpgroup executes it (n a multiple of 8).
+template <int n> __device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
+}
+template <int n> __device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
+}
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }

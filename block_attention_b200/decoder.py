@@ -46,6 +46,34 @@ class DecodeState:
         self.B, self.cap = B, cap
 
 
+class PagedState:
+    """The same state with the cache in pages: pools [L, pages, Hkv, page_size,
+    hd] (k and v) and a page table [B, max_pages].  The first ``shared`` tokens
+    (whole pages of them) lie in pages that every sequence's table names."""
+
+    def __init__(self, model: "TinyDecoder", B: int, cap: int, page_size: int, shared: int = 0):
+        dev = model.device
+        self.max_pages = -(-cap // page_size)
+        common = shared // page_size
+        own = self.max_pages - common
+        shape = (model.L, common + B * own, model.Hkv, page_size, model.hd)
+        self.k = torch.zeros(shape, dtype=model.dtype, device=dev)
+        self.v = torch.zeros(shape, dtype=model.dtype, device=dev)
+        head = torch.arange(common, dtype=torch.int32).expand(B, common)
+        tail = common + torch.arange(B * own, dtype=torch.int32).view(B, own)
+        self.table = torch.cat([head, tail], 1).contiguous().to(dev)
+        self.ctx_lens = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.B, self.cap, self.prefix = B, cap, common * page_size
+
+    def first(self) -> "PagedState":
+        """Sequence 0 of this state alone, over the same pools."""
+        st = object.__new__(PagedState)
+        st.__dict__.update(self.__dict__)
+        st.B, st.table, st.ctx_lens, st.prefix = 1, self.table[:1], self.ctx_lens[:1], 0
+        return st
+
+
 class TinyDecoder:
     """Random-init Qwen3-style decoder on the GPU, in FP32 or BF16.
 
@@ -98,8 +126,12 @@ class TinyDecoder:
             h = ba.rmsnorm(x, lw["attn_norm"], self.eps)
             qkv = ba.linear(h, lw["qkv"][view])
             ba.qkv_rope(qkv, st.ctx_lens, B, R, Hq, Hkv, hd, self.theta, q=q, k=kb[l], v=vb[l])
-            att = ba.block_attn(q, kb[l], vb[l], st.k[l], st.v[l], st.ctx_lens, mode,
-                                err=st.err)
+            if isinstance(st, PagedState):
+                att = ba.paged_block_attn(q, kb[l], vb[l], st.k[l], st.v[l], st.table,
+                                          st.ctx_lens, mode, shared_prefix=st.prefix, err=st.err)
+            else:
+                att = ba.block_attn(q, kb[l], vb[l], st.k[l], st.v[l], st.ctx_lens, mode,
+                                    err=st.err)
             ba.linear(att.view(rows, Hq * hd), lw["o"][view], residual=x, out=x)
             h = ba.rmsnorm(x, lw["ffn_norm"], self.eps)
             a = ba.swiglu(ba.linear(h, lw["gu"]))
@@ -108,7 +140,11 @@ class TinyDecoder:
         return ba.linear(h, self.lm_head), kb, vb
 
     def commit(self, st: DecodeState, kb, vb, n_emit: torch.Tensor):
-        ba.kv_commit(st.k, st.v, kb, vb, st.ctx_lens, n_emit, err=st.err)
+        if isinstance(st, PagedState):
+            ba.paged_append(kb, vb, st.k, st.v, st.table, st.ctx_lens, n_rows=n_emit,
+                            advance=True, err=st.err)
+        else:
+            ba.kv_commit(st.k, st.v, kb, vb, st.ctx_lens, n_emit, err=st.err)
 
     def check(self, st: DecodeState):
         e = int(st.err.item())
@@ -116,8 +152,12 @@ class TinyDecoder:
             raise ba.OrthrusError("device error word", e)
 
     # ------------------------------------------------------------ prefill
-    def prefill(self, prompts, cap: int, chunk: int = 32):
-        """Causal AR pass over every prompt in blocks of ``chunk`` rows.
+    def prefill(self, prompts, cap: int, chunk: int = 32, page_size: int | None = None,
+                shared: int = 0):
+        """Causal AR pass over every prompt in blocks of ``chunk`` rows.  With
+        ``page_size`` the cache is paged, and of the first ``shared`` tokens,
+        which all prompts must have in common, whole pages are computed and
+        kept once.
 
         Returns the state (cache holding each prompt), the first generated
         token per sequence (host int32 [B]) and its log-probability (host
@@ -128,11 +168,30 @@ class TinyDecoder:
         lens = np.array([len(p) for p in prompts], np.int64)
         if lens.min() < 1 or lens.max() + chunk > cap:
             raise ValueError("prompt lengths must lie in [1, cap - chunk]")
+        if page_size is None:
+            if shared:
+                raise ValueError("a shared prefix needs a paged cache")
+            st = DecodeState(self, B, cap)
+        else:
+            if shared and (lens.min() <= shared or
+                           any(list(p[:shared]) != list(prompts[0][:shared]) for p in prompts)):
+                raise ValueError("every prompt must start with the shared tokens and go on")
+            st = PagedState(self, B, cap, page_size, shared)
+            if st.prefix:
+                head = st.first()
+                for c0 in range(0, st.prefix, chunk):
+                    R = min(chunk, st.prefix - c0)
+                    t = torch.tensor([list(prompts[0][c0:c0 + R])], dtype=torch.int32)
+                    _, kb, vb = self.forward(head, t.to(self.device), AR_VIEW)
+                    self.commit(head, kb, vb, torch.full((1,), R, dtype=torch.int32,
+                                                         device=self.device))
+                st.ctx_lens.fill_(st.prefix)
+                prompts = [p[st.prefix:] for p in prompts]
+                lens = lens - st.prefix
         nchunks = int(-(-lens.max() // chunk))
         toks = np.zeros((B, nchunks * chunk), np.int32)
         for b, p in enumerate(prompts):
             toks[b, :len(p)] = p
-        st = DecodeState(self, B, cap)
         first = np.zeros(B, np.int32)
         first_lp = np.zeros(B, np.float32)
         last_chunk, last_row = (lens - 1) // chunk, (lens - 1) % chunk
@@ -152,12 +211,14 @@ class TinyDecoder:
         return st, first, first_lp
 
     # ---------------------------------------------------------- greedy AR
-    def greedy(self, prompts, n_new: int, cap: int | None = None, logprob: bool = False):
+    def greedy(self, prompts, n_new: int, cap: int | None = None, logprob: bool = False,
+               page_size: int | None = None, shared: int = 0):
         """Plain greedy autoregressive decoding, one token per forward:
         int32 [B, n_new] (the first token comes from the prefill); with
-        ``logprob`` also each chosen token's log-probability, float32 [B, n_new]."""
+        ``logprob`` also each chosen token's log-probability, float32 [B, n_new].
+        ``page_size`` and ``shared`` as in prefill."""
         cap = cap or max(len(p) for p in prompts) + n_new + 64
-        st, first, first_lp = self.prefill(prompts, cap)
+        st, first, first_lp = self.prefill(prompts, cap, page_size=page_size, shared=shared)
         B = st.B
         out = torch.empty(n_new, B, dtype=torch.int32, device=self.device)
         out[0].copy_(torch.from_numpy(first))
@@ -175,26 +236,40 @@ class TinyDecoder:
         return (toks, lp.t().contiguous().cpu().numpy()) if logprob else toks
 
     def sample_ar(self, prompts, n_new: int, temperature: float, seed: int,
-                  cap: int | None = None) -> np.ndarray:
+                  cap: int | None = None, top_k: int | None = None,
+                  top_p: float | None = None, min_p: float | None = None,
+                  page_size: int | None = None, shared: int = 0) -> np.ndarray:
         """Plain autoregressive sampling at ``temperature``, one token per
         forward (the first token is the prefill's greedy one, as in the
-        loop): int32 [B, n_new].  Step t uses Philox step t of ``seed``."""
+        loop): int32 [B, n_new].  Step t uses Philox step t of ``seed``; with
+        any of top_k, top_p and min_p it draws from the filtered distribution
+        with row t of the uniforms that ``seed`` gives.  ``page_size`` and
+        ``shared`` as in prefill."""
         cap = cap or max(len(p) for p in prompts) + n_new + 64
-        st, first, _ = self.prefill(prompts, cap)
+        st, first, _ = self.prefill(prompts, cap, page_size=page_size, shared=shared)
         B = st.B
         out = torch.empty(n_new, B, dtype=torch.int32, device=self.device)
         out[0].copy_(torch.from_numpy(first))
         ones = torch.ones(B, dtype=torch.int32, device=self.device)
+        filtered = not (top_k is None and top_p is None and min_p is None)
+        if filtered:
+            u = torch.from_numpy(np.random.default_rng(seed).random((n_new, B), np.float32)).to(
+                self.device)
         for t in range(1, n_new):
             logits, kb, vb = self.forward(st, out[t - 1].view(B, 1), AR_VIEW)
-            ba.vocab_sample(logits, temperature, seed, t, idx=out[t])
+            if filtered:
+                ba.vocab_sample_filtered(logits, u[t], temperature=temperature, top_k=top_k,
+                                         top_p=top_p, min_p=min_p, idx=out[t], err=st.err)
+            else:
+                ba.vocab_sample(logits, temperature, seed, t, idx=out[t])
             self.commit(st, kb, vb, ones)
         self.check(st)
         return out.t().contiguous().cpu().numpy()
 
     # ----------------------------------------------------- consensus loop
     def consensus(self, prompts, n_new: int, blk: int = 32, draft_fn=None,
-                  cap: int | None = None, temperature: float = 0.0, seed: int = 0):
+                  cap: int | None = None, temperature: float = 0.0, seed: int = 0,
+                  page_size: int | None = None, shared: int = 0):
         """The Orthrus loop: int32 [B, n_new] tokens and per-round stats.
 
         ``draft_fn(counts, d)`` may replace the diffusion drafts d (device
@@ -205,9 +280,9 @@ class TinyDecoder:
         probability min(1, p_j(d_j) / q_j(d_j)) and draws the correction from
         normalize(max(0, p - q)); round r uses Philox step r of ``seed``.
         Sequences that reach n_new tokens stop committing; the loop ends when
-        all have."""
+        all have.  ``page_size`` and ``shared`` as in prefill."""
         cap = cap or max(len(p) for p in prompts) + n_new + 2 * blk
-        st, first, _ = self.prefill(prompts, cap)
+        st, first, _ = self.prefill(prompts, cap, page_size=page_size, shared=shared)
         B = st.B
         out = [[int(f)] for f in first]
         counts = np.ones(B, np.int64)

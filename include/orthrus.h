@@ -285,6 +285,45 @@ int orthrus_vocab_sample(int32_t dtype, const void* logits, int32_t rows, int32_
                          int32_t* idx, float* logprob, float* lse, void* workspace,
                          size_t workspace_bytes, orthrus_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Sampling with filters, from given uniforms, per row r:
+ *   w_i = exp((x_i - max x) / T)           T = temperature[r]
+ *   order: x descending, index ascending on ties (NaN counts as -inf)
+ *   top-k: the first top_k[r] of the order                      (<= 0: all)
+ *   top-p: the shortest prefix of those whose mass is >= top_p[r] times
+ *          theirs, at least one                                 (>= 1: all)
+ *   min-p: those with w_i >= min_p[r]                           (<= 0: all)
+ *   idx[r]     = the first kept index j, in vocabulary order, with
+ *                sum_{kept i <= j} w_i > u[r] * sum_kept w_i
+ *   logprob[r] = log(w_idx / sum_kept w)                         (nullable)
+ * u float in [0, 1) (clamped to [0, 1]; NaN as 0; at 1 the last kept index with
+ * any weight).  T == 0 takes the largest logit, lowest index, logprob 0; with a
+ * +inf logit only those have weight.  A row without any value above -inf gives
+ * idx 0 and logprob NaN.  A temperature that is negative, infinite or NaN sets
+ * err (nullable) to ORTHRUS_EINVAL and leaves its row's outputs alone.
+ * temperature, top_k, top_p and min_p are device arrays [rows], each nullable
+ * (T = 1, filter off).  Weights are FP64, summed exactly in 64-bit fixed
+ * point of 62 - ceil(log2 vocab) bits, at most 52, after the point (a smaller
+ * weight counts as zero), so ties and borders do not depend on the run.  rows <= 65535, vocab <= 2^24.  One
+ * launch, one thread-block cluster a row; no workspace.
+ * ---------------------------------------------------------------------- */
+typedef struct orthrus_filter_args {
+  int32_t dtype;        /* of logits */
+  int32_t rows, vocab;
+  int64_t row_stride;   /* elements, >= vocab */
+  const void* logits;
+  const float* u;       /* [rows] */
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* idx;         /* out [rows] */
+  float* logprob;       /* out [rows], nullable */
+  int32_t* err;
+} orthrus_filter_args;
+
+int orthrus_vocab_sample_filtered(const orthrus_filter_args* a, orthrus_stream_t stream);
+
 /* Log-probability of a chosen token per row at temperature T:
  *   lse[r]     = log sum_k exp(logits[r, k] / T)
  *   logprob[r] = logits[r, idx[r]] / T - lse[r]

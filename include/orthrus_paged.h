@@ -1,0 +1,215 @@
+/* orthrus_paged.h -- C ABI of the paged K/V cache: rotary positions in the
+ * variants that served models use, rows appended to pages with the rotation
+ * on the way, and the round's block attention over pages, with the first keys
+ * of a batch shared by all its sequences.
+ *
+ * The pages the method comes from describe one dense cache per sequence
+ * (cjcn.com.cn explainer of "Orthrus", §二 and §七); paging changes where a row
+ * lies, never what a view computes.
+ *
+ * Pools.  k_pages and v_pages are [pages, Hkv, page_size, D]: page x holds, for
+ * every kv-head, page_size consecutive positions of one sequence.  page_table
+ * is int32 [B, max_pages] on the device: position p of sequence b lies in page
+ * page_table[b, p / page_size] at slot p % page_size.  Entries past a
+ * sequence's last position are never read.
+ *
+ * Conventions are those of orthrus.h: caller-owned device pointers, calls
+ * asynchronous on `stream`, host-checkable errors returned before any launch,
+ * device-only errors (a length out of range, a page id outside [0, pages))
+ * recorded in the optional error word with the writes they concern skipped,
+ * no allocation, no synchronisation.  A page id outside the pool is never
+ * dereferenced.
+ */
+#ifndef ORTHRUS_PAGED_H
+#define ORTHRUS_PAGED_H
+
+#include "orthrus.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * A head's first `rot` values (rot even, <= D) are rotated pair by pair by the
+ * angle t = pos * inv_freq[i], i < rot/2; the rest pass through:
+ *   y_a = mscale (x_a cos t - x_b sin t),  y_b = mscale (x_b cos t + x_a sin t)
+ * with (a, b) = (i, i + rot/2) in the half layout and (2i, 2i + 1) in the
+ * interleaved one.  `inverse` turns by -t: with the same mscale it is the
+ * gradient of the call with respect to x.  Angles are FP64, their scaled
+ * cosine and sine are rounded to FP32, the rotation is FP32 and each result
+ * is rounded once to the tensor's type.
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  ORTHRUS_ROPE_HALF = 0,
+  ORTHRUS_ROPE_INTERLEAVED = 1
+} orthrus_rope_layout;
+
+typedef enum {
+  ORTHRUS_ROPE_PLAIN = 0,  /* f_i = theta^(-2i/rot), mscale 1 */
+  ORTHRUS_ROPE_LINEAR = 1, /* f_i / factor (position interpolation) */
+  ORTHRUS_ROPE_NTK = 2,    /* theta -> theta * factor^(rot/(rot-2)); rot >= 4 */
+  /* by turns over the trained context, n_i = original_ctx f_i / (2 pi):
+   * n <= low: f_i / factor; n >= high: f_i; between, linear in n */
+  ORTHRUS_ROPE_BANDS = 3,
+  /* YaRN: f_i / factor above index c(low), f_i below c(high), linear in i
+   * between (c(n) = rot ln(original_ctx / (2 pi n)) / (2 ln theta), rounded
+   * outwards and kept in [0, rot-1]; a ramp of width 0 counts as 0.001);
+   * mscale = 0.1 ln(factor) + 1 unless the given mscale is > 0 */
+  ORTHRUS_ROPE_YARN = 4
+} orthrus_rope_scaling_kind;
+
+typedef struct orthrus_rope_scaling {
+  int32_t kind;        /* orthrus_rope_scaling_kind */
+  double factor;       /* >= 1: stretch of the context */
+  double original_ctx; /* BANDS, YARN: length the frequencies were trained at, > 0 */
+  double low, high;    /* BANDS, YARN: 0 < low < high, in turns */
+  double mscale;       /* YARN: > 0 replaces the default factor; 0 = default */
+} orthrus_rope_scaling;
+
+/* Host only: inv_freq[0 .. rot/2) (host memory) and *mscale for these
+ * settings (scaling NULL = plain).  theta > 1.  ORTHRUS_EINVAL otherwise. */
+int orthrus_rope_freqs(int32_t rot, double theta, const orthrus_rope_scaling* scaling,
+                       double* inv_freq, double* mscale);
+
+typedef struct orthrus_rope_args {
+  int32_t dtype;
+  int32_t layout;      /* orthrus_rope_layout */
+  int32_t rows, H, D;  /* rows >= 0 (0: no-op), D <= 1024 */
+  int32_t rot;         /* even, 0 <= rot <= D */
+  int32_t inverse;     /* 0 or 1 */
+  double mscale;       /* finite */
+  const void* x;       /* element (r, h, d) at x[r * x_row_stride + h * x_head_stride + d] */
+  int64_t x_row_stride, x_head_stride; /* elements, >= 0 */
+  void* out;           /* the same form; out == x with equal strides rotates in place,
+                          any other overlap is not allowed */
+  int64_t out_row_stride, out_head_stride;
+  const int32_t* positions; /* [rows] device, any sign */
+  const double* inv_freq;   /* [rot/2] device (NULL if rot == 0) */
+} orthrus_rope_args;
+
+int orthrus_rope(const orthrus_rope_args* a, orthrus_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Append K/V rows to a paged cache, rotated on the way.
+ *
+ * Row j of sequence b goes to position ctx_lens[b] + j, its K (and the row's
+ * queries, if given) rotated to that position:
+ *   k_pages[page, g, slot, :] = RoPE(k[r, g, :]),  v_pages[..] = v[r, g, :]
+ *   q_out[r, h, :]            = RoPE(q[r, h, :])
+ * Rows come in one of two forms:
+ *   - blocks (row_starts NULL): row r = b * blk + j, rows == B * blk; with
+ *     n_rows (device [B]) only rows j < n_rows[b] are taken -- with n_emit of
+ *     a consensus, layers > 1, rot 0 and advance this is the commit of a
+ *     round (orthrus_kv_commit) into pages;
+ *   - ragged (row_starts, device int32 [B + 1], ascending from 0): rows
+ *     [row_starts[b], row_starts[b+1]) belong to sequence b.  Rows at or past
+ *     row_starts[B] are left alone.
+ * Nothing else is written: not the other slots of a page, not q_out rows that
+ * are not taken.  A row whose position lies outside the table
+ * (ORTHRUS_ECAPACITY), whose page id lies outside the pool (ORTHRUS_EINVAL),
+ * or whose sequence has a negative length or an n_rows outside [0, blk]
+ * (ORTHRUS_ECAPACITY) is not written.  Two rows with the same page and slot
+ * leave one of them, or a mix.
+ *
+ * advance: ctx_lens[b] += rows taken, once every row has been read, for each
+ * sequence all of whose rows were written.  Needs the workspace
+ * (orthrus_paged_append_workspace() bytes, zeroed once, left zero; one call
+ * at a time per buffer, as for orthrus_kv_commit).
+ * ---------------------------------------------------------------------- */
+typedef struct orthrus_append_args {
+  int32_t dtype;
+  int32_t layers;      /* >= 1; q only with 1 */
+  int32_t B;           /* sequences, >= 0 */
+  int32_t blk;         /* rows of a block (row_starts NULL), >= 0 */
+  int32_t rows;        /* rows of k, v and q in one layer (0: no-op) */
+  int32_t Hq, Hkv, D;  /* Hq is 0 without q; D <= 1024 */
+  int32_t page_size, pages, max_pages; /* each >= 1 */
+  int32_t rot, layout; /* rot 0: no rotation */
+  int32_t advance;
+  double mscale;
+  const void* k;       /* element (l, r, g, d) at k[l*k_layer_stride + r*k_row_stride +
+                          g*k_head_stride + d]; strides in elements, >= 0 */
+  const void* v;
+  const void* q;       /* nullable */
+  int64_t k_layer_stride, k_row_stride, k_head_stride;
+  int64_t v_layer_stride, v_row_stride, v_head_stride;
+  int64_t q_row_stride, q_head_stride;
+  void* q_out;         /* [rows, Hq, D] dense */
+  void* k_pages;       /* layer l at k_pages + l * pages_layer_stride */
+  void* v_pages;
+  int64_t pages_layer_stride; /* elements, >= pages*Hkv*page_size*D if layers > 1 */
+  const int32_t* page_table;  /* [B, max_pages] */
+  int32_t* ctx_lens;          /* [B] device; written only with advance */
+  const int32_t* n_rows;      /* nullable, blocks only */
+  const int32_t* row_starts;  /* nullable */
+  const double* inv_freq;     /* [rot/2] device (NULL if rot == 0) */
+  int32_t* err;
+  void* workspace;
+  size_t workspace_bytes;
+} orthrus_append_args;
+
+size_t orthrus_paged_append_workspace(const orthrus_append_args* a);
+int orthrus_paged_append(const orthrus_append_args* a, orthrus_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Block attention over pages, one layer: orthrus_block_attn's two views with
+ * the cache in pages.
+ *
+ * With k_blk / v_blk: keys are positions [0, n), n = ctx_lens[b], from the
+ * pages, then the blk block rows; row i sees every key (BIDIR_BLOCK) or the
+ * first n + i + 1 (CAUSAL_VERIFY), as in orthrus_block_attn.
+ * Without (both NULL): the block's own rows have been appended already and
+ * n counts them; row i sees keys [0, n) or the first n - blk + i + 1.  A row
+ * that sees no key gives zeros.
+ *
+ * shared_prefix = P > 0: the first P keys are common to the batch, and are
+ * read once for all its sequences, through row 0 of page_table.  A sequence
+ * whose first row sees (or, bidirectional and without block rows, whose rows
+ * before the block number) fewer than P keys -- n < P with block rows,
+ * n - blk < P without -- reads all its keys through its own row; the others
+ * read positions >= P through their own row and need no valid entries below
+ * it.  P need not be a multiple of the page size.
+ *
+ * A NaN or infinity in a K or V row reaches exactly the rows that see it.
+ * Slots past a sequence's length may hold anything.
+ *
+ * Arithmetic as orthrus_block_attn: F32 -> FP32 on CUDA cores, row-invariant
+ * between calls with equal max_ctx, B, Hq and Hkv; BF16 ->
+ * tcgen05 tiles with FP32 accumulation, the weights rounded to bf16 for the
+ * product with V (relative 2^-8 each, as its operands are).
+ * A sequence with a length outside [0, max_ctx] (ORTHRUS_ECAPACITY) or a page
+ * id outside the pool among those read for it (ORTHRUS_EINVAL) keeps its old
+ * output rows.
+ * Limits: D 64 or 128, blk <= 32, (Hq/Hkv) * blk <= 128, page_size a power of
+ * two in [16, 256].
+ * ---------------------------------------------------------------------- */
+typedef struct orthrus_paged_attn_args {
+  int32_t dtype, mask_mode; /* orthrus_mask_mode */
+  int32_t B, Hq, Hkv, D, blk;
+  int32_t page_size, pages, max_pages;
+  int32_t max_ctx;       /* host bound on every ctx_lens[b], <= max_pages * page_size */
+  int32_t shared_prefix; /* P, 0 <= P <= max_ctx */
+  float scale;           /* finite, > 0 */
+  const void* q;         /* [B, blk, Hq, D] */
+  const void* k_blk;     /* [B, blk, Hkv, D], or NULL with v_blk */
+  const void* v_blk;
+  const void* k_pages;   /* [pages, Hkv, page_size, D] */
+  const void* v_pages;
+  const int32_t* page_table; /* [B, max_pages] */
+  const int32_t* ctx_lens;   /* [B] device */
+  void* out;             /* [B, blk, Hq, D] */
+  int32_t* err;          /* nullable */
+  void* workspace;       /* orthrus_paged_attn_workspace() bytes, 256-byte aligned; its
+                            contents before and after a call do not matter */
+  size_t workspace_bytes;
+} orthrus_paged_attn_args;
+
+size_t orthrus_paged_attn_workspace(const orthrus_paged_attn_args* a);
+int orthrus_paged_attn(const orthrus_paged_attn_args* a, orthrus_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* ORTHRUS_PAGED_H */
