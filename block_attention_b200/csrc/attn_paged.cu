@@ -7,31 +7,41 @@
 // than 2^8, partial (m, l, O) of different key ranges merged by
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,  M = max_s m_s.
 //
-// Work.  One unit is one 128-row query tile against one key range:
-//   - prefix units (kv-head g, row tile t): the rows of ns = 128 / (G blk)
-//     consecutive sequences packed into one tile, against keys [0, P) of row
-//     0's pages -- with one token a sequence the whole batch shares one read
-//     of the prefix instead of one read a sequence;
-//   - tail units (sequence b, kv-head g): the sequence's G blk rows against
-//     its own keys (from P if it shares the prefix) and the block rows.
-// The units' tiles, W in all, form one sequence that is dealt out evenly: CTA
-// c of C (one per SM) takes tiles [c chunk, (c + 1) chunk), crossing unit
-// boundaries, so a ragged batch loads every SM alike whatever its lengths.  A
-// unit that lies in one CTA and has no prefix is normalised and written
-// straight to the output; every other piece leaves a partial (O, m, l) in the
-// workspace and a second kernel merges them in tile order, so the result
-// depends on the lengths only, not on timing.
+// Work.  A unit is a set of query rows against a range of keys:
+//   - prefix units: the rows of ns = 128 / (G blk) consecutive sequences packed
+//     into one 128-row tile, against keys [0, P) of row 0's pages.  Row tiles
+//     go in pairs ("wide", 256 rows: one warpgroup each, every K/V tile serves
+//     both), the last of an odd number alone;
+//   - tail units (sequence b, kv-head g): the sequence's G blk rows against its
+//     own keys (from P if it shares the prefix) and the block rows.  With at
+//     most 64 (32) rows the row tile holds 2 (4) copies of them, and each copy
+//     takes its own 64 (32) keys of a tile, so that all four warps of a
+//     warpgroup share the exponentials.
+// The units' tiles, with kOverhead added to each unit for its start and end,
+// form one sequence that is dealt out evenly: CTA c of C (one per SM) takes
+// [c chunk, (c + 1) chunk), crossing unit boundaries, so a ragged batch loads
+// every SM alike whatever its lengths.  A unit that lies in one CTA and has no
+// prefix is normalised and written straight to the output; every other piece
+// leaves a partial (O, m, l) in the workspace and a second kernel merges them in
+// tile order, so the result depends on the lengths only, not on timing.
 //
 // Per CTA (12 warps):
-//   warp 0       K producer: lane i of a tile's boxes loads one page's rows of
-//                one 64-dim half (the page ids of the next tile are read while
-//                this one waits), 2-stage ring
-//   warp 1       MMA issuer (one thread), as in attn_tc.cu
-//   warp 2       V producer, like warp 0
+//   warp 0       K/V producer: a ring of five 32 KB slots, filled in the order
+//                the tiles are used (K0 K1 V0 K2 V1 ..); each lane loads one
+//                page's rows of one 64-dim half, the page ids two tiles ahead
+//   warp 1       MMA issuer (one thread)
 //   warp 3       Q tiles
-//   warps 4..11  softmax, two warpgroups taking turns on the tiles
-// Producers run ahead over unit boundaries.  The first warpgroup hands
-// registers to the two softmax ones (72 + 2 x 216 = 3 x 168 a thread).
+//   warps 4..11  softmax, two warpgroups X = 0, 1; a wide unit's row tile X
+//                belongs to warpgroup X, otherwise they take turns on the tiles
+// S(u) = Q K(u)^T goes to the warpgroup's own 128 TMEM columns; P(u) replaces
+// the upper half of S(u) as bf16 and is the A operand of O_X += P(u) V(u)
+// straight from tensor memory, which leaves shared memory to the ring.  The
+// next S of a warpgroup is issued behind its P V, so one commit says that both
+// are done and no further barriers guard the buffers.  Producers run ahead over
+// unit boundaries.  The first warpgroup hands registers to the two softmax
+// ones (72 + 2 x 216 = 3 x 168 a thread).
+// TMEM (512 columns): S_0/P_0 [0,128) S_1/P_1 [128,256) O_0 [256,256+D) O_1
+// after it.
 //
 // NaN and infinities.  Scores of keys a row may not see are replaced, never
 // multiplied; V rows past the keys are zeroed in shared memory.  Keys that
@@ -46,6 +56,7 @@
 #include <math.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "attn_paged.cuh"
 #include "common.cuh"
@@ -56,27 +67,30 @@ namespace {
 
 constexpr int kRows = 128;  // UMMA M
 constexpr int kTile = 128;  // keys per tile
-constexpr int kStages = 2;
+constexpr int kSlots = 5;   // ring of K and V tiles
 constexpr int kThreads = 384;
-constexpr int kTmemCols = 512;  // S0 [0,128) S1 [128,256) O_0 [256,256+D) O_1 after it
+constexpr int kTmemCols = 512;
 constexpr int kOCol = 256;
 constexpr float kLazyThresh = 8.f;  // log2 units
 constexpr int kFlagRing = 8;        // segments whose flags may be alive at once
-constexpr int kMinChunk = 2;        // tiles a CTA takes at least
+constexpr int kOverhead = 2;        // a unit's start and end, in tiles
+constexpr int kMinChunk = 4;        // tiles and overheads a CTA takes at least
 constexpr int kMergeRows = 8;       // query rows of one merging CTA
 
-constexpr int kHalfTile = kTile * 128;
-constexpr int kQBytes = 2 * kRows * 128;
-constexpr int kStageBytes = 4 * kHalfTile;
-constexpr int kRingOff = kQBytes;
-constexpr int kPBytes = 2 * kRows * 128;
-constexpr int kPOff = kRingOff + kStages * kStageBytes;
-constexpr int kBarOff = kPOff + 2 * kPBytes;
-constexpr int kNumBars = 13 + 4 * kStages;
+constexpr int kHalfTile = kTile * 128;      // one 64-dim half of a K or V tile (16 KB)
+constexpr int kSlotBytes = 2 * kHalfTile;
+constexpr int kQBytes = 2 * kRows * 128;    // one row tile
+constexpr int kXchOff = kQBytes;            // (m, l) exchange and copy sums: the second
+constexpr int kSumOff = kXchOff + 2048;     //   row tile's space, which only wide units
+                                            //   (always before narrow ones) load
+constexpr int kRingOff = 2 * kQBytes;
+constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+constexpr int kNumBars = 9 + 2 * kSlots;
 constexpr int kMiscOff = kBarOff + kNumBars * 8;
 // TMEM address, abort flag, start of the walk, scan words, segment flags
 constexpr int kSmemBytes = kMiscOff + 256 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+static_assert(kSumOff + 2 * 4 * kRows * 16 <= kRingOff, "copy sums fit");
 
 struct __align__(64) PagedParams {
   CUtensorMap tm_qp;  // 3D (D, Hq, B*blk), box (64, G, ns*blk)
@@ -91,13 +105,15 @@ struct __align__(64) PagedParams {
   const __nv_bfloat16* v_blk;  // NULL: the block's rows are in the pages
   __nv_bfloat16* out;
   int32_t* err;
-  // workspace: [0] chunk, [1] prefix tiles, [2..] tail tiles before each sequence
+  // workspace: [0] chunk, [1] prefix length in the schedule, [2..] the same of
+  // one kv-head's tails before each sequence
   int32_t* head;
-  float2* ml_p;   // (m, l) of the prefix partials [slot][128]
-  float* o_p;     // their O, [slot][D/4][128][4]
+  float2* ml_p;   // (m, l) of the prefix partials [slot][256]
+  float* o_p;     // their O, [slot][D/4][256][4]
   float2* ml_t;   // the same of the tail partials, rows per slot = G*blk
   float* o_t;
-  int B, Hq, Hkv, G, blk, rowsT, ns, Tq, Kp, P, page_size, pages, max_pages, max_ctx, causal;
+  int B, Hq, Hkv, G, blk, rowsT, copies, ns, Tq, Tw, Kp, P;
+  int page_size, pages, max_pages, max_ctx, causal;
   float scale_log2;
 };
 
@@ -105,18 +121,14 @@ struct Bars {
   uint32_t base;
   __device__ uint32_t at(int i) const { return base + 8 * i; }
   __device__ uint32_t q_full() const { return at(0); }
-  __device__ uint32_t q_free() const { return at(1); }  // every S of the segment is done
-  __device__ uint32_t o_free() const { return at(2); }  // O of the segment has been read
+  __device__ uint32_t q_free() const { return at(1); }    // every S of the segment is done
+  __device__ uint32_t o_free() const { return at(2); }    // O of the segment has been read
   __device__ uint32_t seg_done() const { return at(3); }  // every P V of the segment is done
   __device__ uint32_t exit_done() const { return at(4); }
-  __device__ uint32_t k_full(int s) const { return at(5 + s); }
-  __device__ uint32_t v_full(int s) const { return at(5 + kStages + s); }
-  __device__ uint32_t k_empty(int s) const { return at(5 + 2 * kStages + s); }
-  __device__ uint32_t v_empty(int s) const { return at(5 + 3 * kStages + s); }
-  __device__ uint32_t s_full(int b) const { return at(5 + 4 * kStages + b); }
-  __device__ uint32_t s_free(int b) const { return at(7 + 4 * kStages + b); }
-  __device__ uint32_t p_full(int b) const { return at(9 + 4 * kStages + b); }
-  __device__ uint32_t pv_done(int b) const { return at(11 + 4 * kStages + b); }
+  __device__ uint32_t s_full(int x) const { return at(5 + x); }  // S_X there, P_X V done
+  __device__ uint32_t p_full(int x) const { return at(7 + x); }  // P_X there
+  __device__ uint32_t full(int s) const { return at(9 + s); }
+  __device__ uint32_t empty(int s) const { return at(9 + kSlots + s); }
 };
 
 __device__ __forceinline__ void record_timeout(int32_t* err, volatile int* abort_flag) {
@@ -142,9 +154,16 @@ __device__ __forceinline__ int tail_tiles(const PagedParams& p, int n) {
   const int own = p.v_blk ? 0 : p.blk;
   return cache_tiles(shares(n, p.P, own) ? p.P : 0, n) + (p.v_blk ? 1 : 0);
 }
+// length of a tail unit in the schedule
+__device__ __forceinline__ int tail_cost(const PagedParams& p, int n) {
+  const int T = tail_tiles(p, n);
+  return T ? T + kOverhead : 0;
+}
 
 struct Seg {
-  int prefix;  // a prefix unit (b is then the row tile)
+  int prefix;  // a prefix unit: b is then its first row tile
+  int wide;    // two row tiles
+  int unit;    // prefix: its index
   int b, g;
   int n;       // context length of the sequence (prefix: P)
   int lo;      // first key
@@ -154,74 +173,214 @@ struct Seg {
   int T;       // tiles of the unit
 };
 
-// Walks a CTA's tiles [pos, end) unit by unit.  Every warp role keeps one.
+// Walks a CTA's share [pos, end) of the schedule unit by unit.  Every warp
+// role keeps one.
 struct Walk {
-  int pos, end, base;  // base: prefix tiles in all
-  int b, g, t;         // next tail tile
+  int pos, end, base;  // base: length of the prefix units
+  int b, g, t;         // next position in the tails: sequence, kv-head, offset in its unit
   __device__ __forceinline__ bool next(const PagedParams& p, Seg& s) {
-    if (pos >= end) return false;
-    if (pos < base) {
-      const int unit = pos / p.Kp;
-      s.prefix = 1;
-      s.g = unit / p.Tq;
-      s.b = unit - s.g * p.Tq;
-      s.t0 = pos - unit * p.Kp;
-      s.T = s.Tc = p.Kp;
-      s.n = p.P;
-      s.lo = 0;
-      s.first = 0;
-    } else {
-      int n, T;
-      for (;;) {
-        if (b >= p.B) return false;  // only if lengths change under the kernel
-        n = p.ctx_lens[b];
-        T = tail_tiles(p, n);
-        if (t < T) break;
-        t = 0;
-        if (T > 0 && g + 1 < p.Hkv) { ++g; break; }
-        g = 0;
-        ++b;
+    for (;;) {
+      if (pos >= end) return false;
+      int off, cost;  // position within the unit, its length
+      if (pos < base) {
+        cost = p.Kp + kOverhead;
+        // every kv-head's pairs of row tiles, then the single ones that are left
+        const int unit = pos / cost, pairs = p.Tq / 2;
+        s.prefix = 1;
+        s.wide = unit < p.Hkv * pairs;
+        s.g = s.wide ? unit / pairs : unit - p.Hkv * pairs;
+        s.b = s.wide ? 2 * (unit - s.g * pairs) : p.Tq - 1;
+        s.unit = unit;
+        off = pos - unit * cost;
+        s.T = s.Tc = p.Kp;
+        s.n = p.P;
+        s.lo = 0;
+      } else {
+        int n;
+        for (;;) {
+          if (b >= p.B) return false;  // only if lengths change under the kernel
+          n = p.ctx_lens[b];
+          cost = tail_cost(p, n);
+          if (t < cost) break;
+          t = 0;
+          if (cost > 0 && g + 1 < p.Hkv) { ++g; break; }
+          g = 0;
+          ++b;
+        }
+        s.prefix = s.wide = 0;
+        s.b = b;
+        s.g = g;
+        s.n = n;
+        s.lo = shares(n, p.P, p.v_blk ? 0 : p.blk) ? p.P : 0;
+        s.Tc = cache_tiles(s.lo, n);
+        s.T = cost - kOverhead;
+        off = t;
       }
-      s.prefix = 0;
-      s.b = b;
-      s.g = g;
-      s.n = n;
-      s.lo = shares(n, p.P, p.v_blk ? 0 : p.blk) ? p.P : 0;
+      const int len = min(cost - off, end - pos);
+      pos += len;
+      if (!s.prefix) t += len;
+      // the unit's first kOverhead positions carry no tile
+      s.t0 = max(0, off - kOverhead);
+      s.U = off + len - kOverhead - s.t0;
+      if (s.U <= 0) continue;
       s.first = s.lo / kTile;
-      s.Tc = cache_tiles(s.lo, n);
-      s.T = T;
-      s.t0 = t;
+      return true;
     }
-    s.U = min(s.T - s.t0, end - pos);
-    pos += s.U;
-    if (!s.prefix) t += s.U;
-    return true;
   }
 };
 
-// Slot of a tail piece.  Without a prefix only the first and the last segment
-// of a CTA can be pieces of a unit; with one every tail unit may leave a
-// partial, and (unit, CTA) steps through the schedule like a staircase, so
-// unit + CTA numbers the pieces without gaps.
-__device__ __forceinline__ int tail_slot(const PagedParams& p, int b, int g, int c,
-                                         bool first_seg) {
-  return p.P > 0 ? b * p.Hkv + g + c : 2 * c + (first_seg ? 0 : 1);
+// Slot of a tail piece that starts at tile t0 of its unit, in CTA c.  Without a
+// prefix a CTA leaves at most two: the end of a unit that began before it and
+// the beginning of one that it does not finish.  With a prefix every tail unit
+// may leave a partial, and (unit, CTA) steps through the schedule like a
+// staircase, so unit + CTA numbers the pieces.
+__device__ __forceinline__ int tail_slot(const PagedParams& p, int b, int g, int c, bool begins) {
+  return p.P > 0 ? b * p.Hkv + g + c : 2 * c + (begins ? 1 : 0);
+}
+
+// Position in the ring's fill order of tile u's K and V, of a segment of U
+// tiles that starts at item it0: K0 K1 V0 K2 V1 .. K(U-1) V(U-2) V(U-1).
+__device__ __forceinline__ int k_item(int it0, int u) { return it0 + (u ? 2 * u - 1 : 0); }
+__device__ __forceinline__ int v_item(int it0, int u, int U) {
+  return it0 + (u + 1 < U ? 2 * u + 2 : 2 * U - 1);
 }
 
 // --------------------------------------------------------------- main kernel
 
-__device__ __forceinline__ void mask_range(uint32_t (&sv)[2][32], int k0, int lo, int hi) {
+// Scores of keys [k0, k0 + 32): those outside [lo, hi) -> -inf
+__device__ __forceinline__ void mask32(uint32_t (&sv)[32], int k0, int lo, int hi) {
 #pragma unroll
-  for (int cb = 0; cb < 2; ++cb)
+  for (int j = 0; j < 32; ++j)
+    if (k0 + j < lo || k0 + j >= hi) sv[j] = __float_as_uint(-INFINITY);
+}
+__device__ __forceinline__ float max32(const uint32_t (&sv)[32]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int k = k0 + 32 * cb + j;
-      if (k < lo || k >= hi) sv[cb][j] = __float_as_uint(-INFINITY);
-    }
+  for (int j = 0; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], __uint_as_float(sv[j]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// weights 2^(s c + nm) of 32 scores as bf16 pairs; adds them to ls
+__device__ __forceinline__ void exp32(const uint32_t (&sv)[32], float c, float nm, float (&ls)[4],
+                                      uint32_t* w) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const float p0 = ptx::ex2(fmaf(__uint_as_float(sv[j]), c, nm));
+    const float p1 = ptx::ex2(fmaf(__uint_as_float(sv[j + 1]), c, nm));
+    ls[(j >> 1) & 3] += p0 + p1;
+    w[j >> 1] = ptx::pack_bf16x2(p0, p1);
+  }
 }
 
 __device__ __forceinline__ bool nonfinite_bf16(uint32_t half) {
   return (half & 0x7f80u) == 0x7f80u;
+}
+
+struct RowState {
+  float m, l;  // running maximum (of the scaled scores, lazily raised) and sum
+};
+
+// New running maximum for a tile whose scaled maximum is ms; returns the factor
+// for what has been accumulated (1 if nothing changes for any row of the warp).
+__device__ __forceinline__ float raise_max(RowState& st, float ms, bool& any) {
+  const bool need = ms > st.m + kLazyThresh;
+  any = __any_sync(0xffffffffu, need);
+  if (!need) return 1.f;
+  const float f = st.m == -INFINITY ? 0.f : ptx::ex2(st.m - ms);
+  st.m = ms;
+  return f;
+}
+
+// Softmax of one tile for the row of this thread: kCols keys from column c0 of
+// the tile, of which the row sees [lo, nv).  Reads S, writes P (zero in the
+// other columns) and returns the factor for O.
+template <int kCols>
+__device__ __forceinline__ float softmax_tile(uint32_t s_addr, int c0, int lo, int nv, float c,
+                                              bool row_ok, RowState& st, bool& rescale) {
+  float f, ls[4] = {0.f, 0.f, 0.f, 0.f};
+  const uint32_t p_addr = s_addr + 64;
+  const bool mask = nv < c0 + kCols || lo > c0;
+  if constexpr (kCols == 128) {
+    // 64 columns at a time, so that no more scores than that are live: both
+    // halves for the maximum, the second kept into its exponentials, the first
+    // read again.  P's words 32..63 may replace S's columns 96..127 as soon as
+    // those are in registers, words 0..31 the columns 64..95.
+    uint32_t a[32], b[32], w[32];
+    ptx::tmem_ld32(s_addr, a);
+    ptx::tmem_ld32(s_addr + 32, b);
+    ptx::tmem_wait_ld();
+    if (mask) { mask32(a, 0, lo, nv); mask32(b, 32, lo, nv); }
+    float mt = fmaxf(max32(a), max32(b));
+    ptx::tmem_ld32(s_addr + 64, a);
+    ptx::tmem_ld32(s_addr + 96, b);
+    ptx::tmem_wait_ld();
+    if (mask) { mask32(a, 64, lo, nv); mask32(b, 96, lo, nv); }
+    mt = fmaxf(mt, fmaxf(max32(a), max32(b)));
+    f = raise_max(st, row_ok ? mt * c : -INFINITY, rescale);
+    const float nm = st.m == -INFINITY ? 0.f : -st.m;
+    exp32(a, c, nm, ls, w);
+    exp32(b, c, nm, ls, w + 16);
+    ptx::tmem_st32(p_addr + 32, w);
+    ptx::tmem_ld32(s_addr, a);
+    ptx::tmem_ld32(s_addr + 32, b);
+    ptx::tmem_wait_ld();
+    if (mask) { mask32(a, 0, lo, nv); mask32(b, 32, lo, nv); }
+    exp32(a, c, nm, ls, w);
+    exp32(b, c, nm, ls, w + 16);
+    ptx::tmem_st32(p_addr, w);
+  } else {
+    uint32_t a[kCols / 32][32];
+    float mt = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < kCols / 32; ++h) ptx::tmem_ld32(s_addr + c0 + 32 * h, a[h]);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int h = 0; h < kCols / 32; ++h) {
+      if (mask) mask32(a[h], c0 + 32 * h, lo, nv);
+      mt = fmaxf(mt, max32(a[h]));
+    }
+    f = raise_max(st, row_ok ? mt * c : -INFINITY, rescale);
+    const float nm = st.m == -INFINITY ? 0.f : -st.m;
+    uint32_t zero[16], w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) zero[j] = 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {  // word groups of 32 keys
+      const int h = g - c0 / 32;   // warp-uniform
+      if (h < 0 || h >= kCols / 32) {
+        ptx::tmem_st16(p_addr + 16 * g, zero);
+        continue;
+      }
+#pragma unroll
+      for (int hh = 0; hh < kCols / 32; ++hh)
+        if (hh == h) exp32(a[hh], c, nm, ls, w);
+      ptx::tmem_st16(p_addr + 16 * g, w);
+    }
+  }
+  st.l = fmaf(st.l, f, (ls[0] + ls[1]) + (ls[2] + ls[3]));
+  return f;
+}
+
+// Sum of the non-finite V elements, zeroed in the tiles, of dim `col` of the
+// block's keys [key, last] in unit tiles [t0, t1).  Rare, and kept out of the way.
+template <int kD>
+__device__ __noinline__ float nonfinite_sum(const PagedParams& p, int b, int g, int n, int key,
+                                            int last, int first, int Tc, int t0, int t1,
+                                            int col) {
+  float sum = 0.f;
+  for (; key <= last; ++key) {
+    const __nv_bfloat16* vr;
+    const int tile = p.v_blk ? Tc : key / kTile - first;
+    if (tile < t0 || tile >= t1) continue;
+    if (p.v_blk) {
+      vr = p.v_blk + ((int64_t)(b * p.blk + key - n) * p.Hkv + g) * kD;
+    } else {
+      const int id = p.table[(int64_t)b * p.max_pages + key / p.page_size];
+      vr = p.v_pages + (((int64_t)id * p.Hkv + g) * p.page_size + key % p.page_size) * kD;
+    }
+    const float x = __bfloat162float(vr[col]);
+    if (!isfinite(x)) sum += x;
+  }
+  return sum;
 }
 
 template <int kD>
@@ -239,32 +398,29 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
   const Bars bars{sbase + kBarOff};
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
-  int* start = reinterpret_cast<int*>(smem + kMiscOff + 8);  // pos, end, base, b, g, t
+  int* start = reinterpret_cast<int*>(smem + kMiscOff + 8);  // b, g, t
   int* scan = reinterpret_cast<int*>(smem + kMiscOff + 32);  // one word a warp
-  volatile int* bad_page = reinterpret_cast<volatile int*>(smem + kMiscOff + 96);
   volatile int* agreed = reinterpret_cast<volatile int*>(smem + kMiscOff + 92);
+  volatile int* bad_page = reinterpret_cast<volatile int*>(smem + kMiscOff + 96);
   volatile int* has_nf = reinterpret_cast<volatile int*>(smem + kMiscOff + 96 + 4 * kFlagRing);
 
   if (threadIdx.x == 0) {
-    *abort_flag = 0;
+    *abort_flag = *agreed = 0;
     ptx::mbar_init(bars.q_full(), 1);
     ptx::mbar_init(bars.q_free(), 1);
     ptx::mbar_init(bars.o_free(), 256);
     ptx::mbar_init(bars.seg_done(), 1);
     ptx::mbar_init(bars.exit_done(), 1);
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bars.k_full(s), 1);
-      ptx::mbar_init(bars.v_full(s), 1);
-      ptx::mbar_init(bars.k_empty(s), 1);
-      ptx::mbar_init(bars.v_empty(s), 1);
-    }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(bars.s_full(s), 1);
-      ptx::mbar_init(bars.s_free(s), 128);
       ptx::mbar_init(bars.p_full(s), 128);
-      ptx::mbar_init(bars.pv_done(s), 1);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      ptx::mbar_init(bars.full(s), 1);
+      ptx::mbar_init(bars.empty(s), 1);
     }
     ptx::fence_mbar_init();
+    start[0] = start[1] = start[2] = 0;
   }
   if (threadIdx.x < kFlagRing) bad_page[threadIdx.x] = has_nf[threadIdx.x] = 0;
   if (warp == 0 && lane == 0) {
@@ -279,251 +435,338 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
 
-  // ---- the schedule: total tail tiles, then where this CTA's share begins
+  // ---- the schedule: its whole length, then where this CTA's share begins.
+  // The first kThreads sequences stay in registers between the two steps.
+  const int base = p.Hkv * p.Tw * (p.Kp + kOverhead);  // Tw: prefix units of a kv-head
+  int pos, end;
   {
-    int mine = 0;
-    for (int b = threadIdx.x; b < p.B; b += kThreads) mine += tail_tiles(p, p.ctx_lens[b]);
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(full_mask, mine, o);
-    if (lane == 0) scan[warp] = mine;
-    __syncthreads();
-    int tail = 0;
-    for (int w = 0; w < kThreads / 32; ++w) tail += scan[w];
-    const int base = p.Hkv * p.Tq * p.Kp;
-    const int W = base + p.Hkv * tail;
-    const int chunk = max(kMinChunk, ceil_div(W, C));
-    const int pos = min(W, c * chunk), end = min(W, pos + chunk);
-    const int want = max(0, pos - base);
-    if (threadIdx.x == 0) {
-      start[0] = pos;
-      start[1] = end;
-      start[2] = base;
-      start[3] = start[4] = start[5] = 0;
-      if (c == 0) {
-        p.head[0] = chunk;
-        p.head[1] = base;
-      }
+    int cost0 = 0, rest = 0;
+    for (int b = threadIdx.x; b < p.B; b += kThreads) {
+      const int n = p.ctx_lens[b];
+      if (c == 0 && (n < 0 || n > p.max_ctx)) set_err(p.err, ORTHRUS_ECAPACITY);
+      if (b < kThreads) cost0 = tail_cost(p, n); else rest += tail_cost(p, n);
     }
+    int inc = cost0;  // inclusive sum over the first kThreads sequences
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(full_mask, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) scan[warp] = inc;
     __syncthreads();
-    int before = 0;  // tail tiles (of one kv-head) before this batch of sequences
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    int off = 0, first = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) off += scan[w];
+      first += scan[w];
+    }
+    int all = first;
+    if (p.B > kThreads) {
+      __syncthreads();
+      rest = __reduce_add_sync(full_mask, rest);
+      if (lane == 0) scan[warp] = rest;
+      __syncthreads();
+      for (int w = 0; w < kThreads / 32; ++w) all += scan[w];
+    }
+    const int W = base + p.Hkv * all;
+    const int chunk = max(kMinChunk, ceil_div(W, C));
+    pos = min(W, c * chunk);
+    end = min(W, pos + chunk);
+    const int want = max(0, pos - base);
+    if (c == 0 && threadIdx.x == 0) {
+      p.head[0] = chunk;
+      p.head[1] = base;
+    }
+    auto place = [&](int b, int at, int cost) {  // `at`: schedule before sequence b
+      if (b < p.B && c == 0) p.head[2 + b] = at;
+      if (cost > 0 && want >= p.Hkv * at && want < p.Hkv * (at + cost)) {
+        const int rem = want - p.Hkv * at;
+        start[0] = b;
+        start[1] = rem / cost;
+        start[2] = rem % cost;
+      }
+    };
+    place(threadIdx.x, off + inc - cost0, cost0);
+    int before = first;
+    for (int b0 = kThreads; b0 < p.B; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
-      const int T = b < p.B ? tail_tiles(p, p.ctx_lens[b]) : 0;
-      int inc = T;
+      const int cost = b < p.B ? tail_cost(p, p.ctx_lens[b]) : 0;
+      inc = cost;
+#pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(full_mask, inc, o);
         if (lane >= o) inc += up;
       }
+      __syncthreads();
       if (lane == 31) scan[warp] = inc;
       __syncthreads();
-      int off = before, all = 0;
+      off = before;
       for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) off += scan[w];
-        all += scan[w];
+        before += scan[w];
       }
-      const int at = off + inc - T;  // tiles before sequence b
-      if (b < p.B && c == 0) p.head[2 + b] = at;
-      if (T > 0 && want >= p.Hkv * at && want < p.Hkv * (at + T)) {
-        const int rem = want - p.Hkv * at;
-        start[3] = b;
-        start[4] = rem / T;
-        start[5] = rem % T;
-      }
-      before += all;
-      __syncthreads();
+      place(b, off + inc - cost, cost);
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  Walk walk{start[0], start[1], start[2], start[3], start[4], start[5]};
-  if (threadIdx.x < 32)  // lengths out of range: reported once
-    if (c == 0)
-      for (int b = lane; b < p.B; b += 32) {
-        const int n = p.ctx_lens[b];
-        if (n < 0 || n > p.max_ctx) set_err(p.err, ORTHRUS_ECAPACITY);
-      }
+  Walk walk{pos, end, base, start[0], start[1], start[2]};
 
   const uint32_t q_s = sbase;
-  auto k_s = [&](int st) { return sbase + kRingOff + st * kStageBytes; };
-  auto v_s = [&](int st) { return sbase + kRingOff + st * kStageBytes + 2 * kHalfTile; };
-  auto p_s = [&](int x) { return sbase + kPOff + x * kPBytes; };
+  auto slot_s = [&](int it) { return sbase + kRingOff + (it % kSlots) * kSlotBytes; };
   Seg s;
 
   if (warp < 4) {
     ptx::reg_dec<72>();
-  if (warp == 0 || warp == 2) {
-    // ================================================== K and V producers
-    const bool is_v = warp == 2;
-    const CUtensorMap* tm = is_v ? &p.tm_v : &p.tm_k;
-    const CUtensorMap* tmb = is_v ? &p.tm_vb : &p.tm_kb;
-    const int box = min(p.page_size, kTile);  // rows of one box
-    const int npg = kTile / box;              // pages a tile touches at most
-    const int mh = lane / npg, mi = lane % npg;  // this lane's half and page of a tile
-    int u = 0;  // tiles issued by this CTA so far
-    bool stop = false;
-    for (int sg = 0; !stop && walk.next(p, s); ++sg) {
-      if (!is_v && lane == 0) bad_page[sg % kFlagRing] = 0;
-      const int32_t* row = p.table + (int64_t)(s.prefix ? 0 : s.b) * p.max_pages;
-      // page of this lane's box of unit tile t: -1 if it holds no key of the unit
-      auto page_of = [&](int t) {
-        if (mh >= halves || t >= s.Tc) return -1;
-        const int k0 = (s.first + t) * kTile + mi * box;
-        if (k0 >= s.n || k0 + box <= s.lo) return -1;
-        return row[k0 / p.page_size];
-      };
-      int id = page_of(s.t0);
-      for (int t = s.t0; t < s.t0 + s.U; ++t, ++u) {
-        const int st = u % kStages;
-        const uint32_t empty = is_v ? bars.v_empty(st) : bars.k_empty(st);
-        const uint32_t bar = is_v ? bars.v_full(st) : bars.k_full(st);
-        const uint32_t dst = is_v ? v_s(st) : k_s(st);
-        const int id_next = t + 1 < s.t0 + s.U ? page_of(t + 1) : -1;
-        if (__any_sync(full_mask, *abort_flag != 0) ||
-            !__all_sync(full_mask, ptx::mbar_wait(empty, ((u / kStages) & 1) ^ 1))) {
-          if (!*abort_flag) record_timeout(p.err, abort_flag);
-          stop = true;
-          break;
+    if (warp == 0) {
+      // ================================================== K/V producer
+      const int box = min(p.page_size, kTile);  // rows of one box
+      const int npg = kTile / box;              // pages a tile touches at most
+      const int mh = lane / npg, mi = lane % npg;  // this lane's half and page of a tile
+      int it = 0;  // items issued by this CTA so far
+      bool stop = false;
+      for (int sg = 0; !stop && walk.next(p, s); ++sg) {
+        if (lane == 0) bad_page[sg % kFlagRing] = 0;
+        __syncwarp();
+        const int32_t* row = p.table + (int64_t)(s.prefix ? 0 : s.b) * p.max_pages;
+        const int t1 = s.t0 + s.U;
+        // first key of this lane's box of unit tile t, and whether it holds keys
+        auto box_key = [&](int t) { return (s.first + t) * kTile + mi * box; };
+        auto has_keys = [&](int t) {
+          const int k0 = box_key(t);
+          return mh < halves && t < s.Tc && k0 < s.n && k0 + box > s.lo;
+        };
+        auto page_of = [&](int t) {
+          return t < t1 && has_keys(t) ? row[box_key(t) / p.page_size] : -1;
+        };
+        // one K or V tile into the next slot
+        auto issue = [&](bool is_v, int t, int id) {
+          const uint32_t bar = bars.full(it % kSlots), dst = slot_s(it);
+          if (__any_sync(full_mask, *abort_flag != 0) ||
+              !__all_sync(full_mask,
+                          ptx::mbar_wait(bars.empty(it % kSlots), ((it / kSlots) & 1) ^ 1))) {
+            if (!*abort_flag) record_timeout(p.err, abort_flag);
+            stop = true;
+            return;
+          }
+          if (t == s.Tc) {  // the block rows
+            if (lane == 0) {
+              ptx::mbar_expect_tx(bar, (uint32_t)(halves * p.blk * 128));
+              for (int h = 0; h < halves; ++h)
+                ptx::tma_load_3d(dst + h * kHalfTile, is_v ? &p.tm_vb : &p.tm_kb, bar, 64 * h,
+                                 s.g, s.b * p.blk);
+            }
+          } else {
+            const bool has = has_keys(t);
+            const bool ok = has && id >= 0 && id < p.pages;
+            if (has && !ok) {
+              bad_page[sg % kFlagRing] = 1;
+              set_err(p.err, ORTHRUS_EINVAL);
+            }
+            const int boxes = __popc(__ballot_sync(full_mask, ok));
+            if (lane == 0) {
+              if (boxes)
+                ptx::mbar_expect_tx(bar, (uint32_t)(boxes * box * 128));
+              else
+                ptx::mbar_arrive(bar);  // nothing to load: every page was refused
+            }
+            __syncwarp();
+            if (ok)
+              ptx::tma_load_2d(dst + mh * kHalfTile + mi * box * 128, is_v ? &p.tm_v : &p.tm_k,
+                               bar, 64 * mh,
+                               (id * p.Hkv + s.g) * p.page_size + box_key(t) % p.page_size);
+          }
+          ++it;
+        };
+        int id0 = page_of(s.t0), id1 = page_of(s.t0 + 1), id2 = page_of(s.t0 + 2);
+        issue(false, s.t0, id0);
+        for (int t = s.t0; t < t1 && !stop; ++t) {
+          const int id3 = page_of(t + 3);
+          if (t + 1 < t1) issue(false, t + 1, id1);
+          if (!stop) issue(true, t, id0);
+          id0 = id1; id1 = id2; id2 = id3;
         }
-        if (t == s.Tc) {  // the block rows
-          if (lane == 0) {
-            ptx::mbar_expect_tx(bar, (uint32_t)(halves * p.blk * 128));
+      }
+      // every issued load must have landed before the CTA exits
+      for (int x = max(0, it - kSlots); x < it; ++x)
+        if (!ptx::mbar_wait(bars.full(x % kSlots), (x / kSlots) & 1))
+          record_timeout(p.err, abort_flag);
+    } else if (warp == 3) {
+      // ================================================== Q tiles
+      if (lane == 0) {
+        int sg = 0;
+        for (; walk.next(p, s); ++sg) {
+          if (*abort_flag || (sg > 0 && !ptx::mbar_wait(bars.q_free(), (sg - 1) & 1))) {
+            if (!*abort_flag) record_timeout(p.err, abort_flag);
+            break;
+          }
+          const int rows = s.prefix ? p.ns * p.rowsT : p.rowsT;
+          const int reps = s.prefix ? 1 + s.wide : p.copies;
+          ptx::mbar_expect_tx(bars.q_full(), (uint32_t)(halves * reps * rows * 128));
+          for (int i = 0; i < reps; ++i) {
+            const uint32_t dst = q_s + (s.prefix ? i * kQBytes : i * (kRows / p.copies) * 128);
+            const int b0 = s.prefix ? (s.b + i) * p.ns : s.b;
             for (int h = 0; h < halves; ++h)
-              ptx::tma_load_3d(dst + h * kHalfTile, tmb, bar, 64 * h, s.g, s.b * p.blk);
+              ptx::tma_load_3d(dst + h * (kRows * 128), s.prefix ? &p.tm_qp : &p.tm_q,
+                               bars.q_full(), 64 * h, s.g * p.G, b0 * p.blk);
           }
-        } else {
-          const int k0 = (s.first + t) * kTile + mi * box;
-          const bool has = mh < halves && k0 < s.n && k0 + box > s.lo;
-          const bool ok = has && id >= 0 && id < p.pages;
-          if (has && !ok && !is_v) {
-            bad_page[sg % kFlagRing] = 1;
-            set_err(p.err, ORTHRUS_EINVAL);
-          }
-          const int boxes = __popc(__ballot_sync(full_mask, ok));
-          __syncwarp();
-          if (lane == 0) {
-            if (boxes)
-              ptx::mbar_expect_tx(bar, (uint32_t)(boxes * box * 128));
-            else
-              ptx::mbar_arrive(bar);  // nothing to load: every page was refused
-          }
-          __syncwarp();
-          if (ok)
-            ptx::tma_load_2d(dst + mh * kHalfTile + mi * box * 128, tm, bar, 64 * mh,
-                             (id * p.Hkv + s.g) * p.page_size + k0 % p.page_size);
         }
-        id = id_next;
+        if (sg > 0 && !ptx::mbar_wait(bars.q_full(), (sg - 1) & 1))
+          record_timeout(p.err, abort_flag);
       }
-    }
-    // every issued load must have landed before the CTA exits
-    for (int x = max(0, u - kStages); x < u; ++x) {
-      const uint32_t bar = is_v ? bars.v_full(x % kStages) : bars.k_full(x % kStages);
-      if (!ptx::mbar_wait(bar, (x / kStages) & 1)) record_timeout(p.err, abort_flag);
-    }
-  } else if (warp == 3) {
-    // ================================================== Q tiles
-    if (lane == 0) {
-      int sg = 0;
-      for (; walk.next(p, s); ++sg) {
-        if (*abort_flag || (sg > 0 && !ptx::mbar_wait(bars.q_free(), (sg - 1) & 1))) {
-          if (!*abort_flag) record_timeout(p.err, abort_flag);
-          break;
-        }
-        const int nb = s.prefix ? p.ns : 1, b0 = s.prefix ? s.b * p.ns : s.b;
-        ptx::mbar_expect_tx(bars.q_full(), (uint32_t)(halves * nb * p.rowsT * 128));
-        for (int h = 0; h < halves; ++h)
-          ptx::tma_load_3d(q_s + h * (kRows * 128), s.prefix ? &p.tm_qp : &p.tm_q,
-                           bars.q_full(), 64 * h, s.g * p.G, b0 * p.blk);
-      }
-      if (sg > 0 && !ptx::mbar_wait(bars.q_full(), (sg - 1) & 1))
-        record_timeout(p.err, abort_flag);
-    }
-  } else {
-    // ================================================== MMA issuer
-    if (lane == 0) {
+    } else if (warp == 1) {
+      // ================================================== MMA issuer
+      // The whole warp walks and waits, so that descriptors and addresses stay
+      // warp-uniform; one elected lane issues.
+      const bool lead = ptx::elect_one();
       const uint32_t id_s = ptx::idesc_bf16(kRows, kTile, false, false);
       const uint32_t id_pv = ptx::idesc_bf16(kRows, kD, false, true);
-      auto s_tile = [&](int u) {
-        const int st = u % kStages;
-#pragma unroll
-        for (int k = 0; k < kD / 16; ++k) {
-          const uint32_t h = k >> 2, kk = k & 3;
-          const uint64_t ad = ptx::sdesc_sw128(q_s + h * (kRows * 128) + kk * 32, 16, 1024);
-          const uint64_t bd = ptx::sdesc_sw128(k_s(st) + h * kHalfTile + kk * 32, 16, 1024);
-          ptx::mma_ss(tmem + (u & 1) * kTile, ad, bd, id_s, k > 0 ? 1u : 0u);
-        }
-        ptx::tc_commit(bars.s_full(u & 1));
-        ptx::tc_commit(bars.k_empty(st));
-      };
-      auto pv_tile = [&](int u, bool fresh) {
-        const int st = u % kStages;
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k) {
-          const uint32_t h = k >> 2, kk = k & 3;
-          const uint64_t ad =
-              ptx::sdesc_sw128(p_s(u & 1) + h * (kRows * 128) + kk * 32, 16, 1024);
-          const uint64_t bd = ptx::sdesc_sw128(v_s(st) + k * 2048, kHalfTile, 1024);
-          ptx::mma_ss(tmem + kOCol + (u & 1) * kD, ad, bd, id_pv, (!fresh || k > 0) ? 1u : 0u);
-        }
-        ptx::tc_commit(bars.pv_done(u & 1));
-        ptx::tc_commit(bars.v_empty(st));
-      };
-      // S of tile u: its buffer's previous scores read, its keys there
-      auto try_s = [&](int u) {
-        if (u > 1 && !ptx::mbar_wait(bars.s_free(u & 1), ((u >> 1) - 1) & 1)) return false;
-        if (!ptx::mbar_wait(bars.k_full(u % kStages), (u / kStages) & 1)) return false;
+      // descriptors of Q and of ring slot 0 as K (K-major) and as V (MN-major:
+      // 8-key groups 1024 B apart, 64-dim halves kHalfTile apart); addresses
+      // advance in their low bits, in units of 16 bytes
+      const uint64_t qd = ptx::sdesc_sw128(q_s, 16, 1024);
+      const uint64_t kd = ptx::sdesc_sw128(sbase + kRingOff, 16, 1024);
+      const uint64_t vd = ptx::sdesc_sw128(sbase + kRingOff, kHalfTile, 1024);
+      auto landed = [&](int it) {
+        if (!ptx::mbar_wait(bars.full(it % kSlots), (it / kSlots) & 1)) return false;
         ptx::tc_fence_after();
-        s_tile(u);
         return true;
       };
-      int u0 = 0;
-      bool ok = true;
-      for (int sg = 0; ok && walk.next(p, s); ++sg) {
-        const int u1 = u0 + s.U;
-        ok = !*abort_flag && ptx::mbar_wait(bars.q_full(), sg & 1);
-        for (int u = u0; ok && u < min(u0 + 2, u1); ++u) ok = try_s(u);
-        if (ok && s.U <= 2) ptx::tc_commit(bars.q_free());
-        // O of the previous segment must have been read
-        if (ok && sg > 0) ok = ptx::mbar_wait(bars.o_free(), (sg - 1) & 1);
-        for (int u = u0; ok && u < u1 && !*abort_flag; ++u) {
-          if (u + 2 < u1) {
-            ok = try_s(u + 2);
-            if (!ok) break;
-            if (u + 3 == u1) ptx::tc_commit(bars.q_free());
-          }
-          ok = ptx::mbar_wait(bars.p_full(u & 1), (u >> 1) & 1) &&
-               ptx::mbar_wait(bars.v_full(u % kStages), (u / kStages) & 1);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          pv_tile(u, u < u0 + 2);
+      // S_x = Q K^T with row tile q and the K tile of item it
+      auto s_tile = [&](int x, int q, int it) {
+        const uint64_t a = qd + (uint64_t)(q * (kQBytes >> 4));
+        const uint64_t b = kd + (uint64_t)((it % kSlots) * (kSlotBytes >> 4));
+        if (lead) {
+#pragma unroll
+          for (int k = 0; k < kD / 16; ++k)  // 64-dim half k / 4, 16-dim step k % 4 in it
+            ptx::mma_ss(tmem + x * kTile, a + (k >> 2) * (kHalfTile >> 4) + (k & 3) * 2,
+                        b + (k >> 2) * (kHalfTile >> 4) + (k & 3) * 2, id_s, k > 0 ? 1u : 0u);
+          ptx::tc_commit(bars.s_full(x));
         }
-        if (ok) ptx::tc_commit(bars.seg_done());
-        u0 = u1;
+        __syncwarp();
+      };
+      // O_x (+)= P_x V, P_x from tensor memory, 16 keys = 8 columns a step
+      auto pv_tile = [&](int x, int it, bool fresh) {
+        const uint64_t b = vd + (uint64_t)((it % kSlots) * (kSlotBytes >> 4));
+        if (lead) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            ptx::mma_ts(tmem + kOCol + x * kD, tmem + x * kTile + 64 + 8 * k, b + k * (2048 >> 4),
+                        id_pv, (!fresh || k > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint32_t bar) {
+        if (lead) ptx::tc_commit(bar);
+        __syncwarp();
+      };
+      auto all = [&](bool v) { return __all_sync(full_mask, v) != 0; };
+      int it0 = 0, x0 = 0;   // items and the turn before this segment
+      int np0 = 0, np1 = 0;  // P tiles taken of each warpgroup
+      bool ok = true;
+      auto p_ready = [&](int x) {
+        if (!ptx::mbar_wait(bars.p_full(x), (x ? np1 : np0) & 1)) return false;
+        if (x) ++np1; else ++np0;
+        ptx::tc_fence_after();
+        return true;
+      };
+      for (int sg = 0; ok && walk.next(p, s); ++sg) {
+        const int U = s.U;
+        ok = all(!*abort_flag && ptx::mbar_wait(bars.q_full(), sg & 1));
+        if (!ok) break;
+        if (s.wide) {
+          ok = all(landed(k_item(it0, 0)));
+          if (!ok) break;
+          s_tile(0, 0, k_item(it0, 0));
+          s_tile(1, 1, k_item(it0, 0));
+          commit(bars.empty(k_item(it0, 0) % kSlots));
+          if (U == 1) commit(bars.q_free());
+          if (sg > 0) ok = all(ptx::mbar_wait(bars.o_free(), (sg - 1) & 1));
+          for (int u = 0; ok && u < U; ++u) {
+            const int vi = v_item(it0, u, U), ki = k_item(it0, u + 1);
+            const bool more = u + 1 < U;
+            ok = all(!*abort_flag && p_ready(0) && landed(vi));
+            if (!ok) break;
+            pv_tile(0, vi, u == 0);
+            if (more) {
+              ok = all(landed(ki));
+              if (!ok) break;
+              s_tile(0, 0, ki);
+            }
+            ok = all(p_ready(1));
+            if (!ok) break;
+            pv_tile(1, vi, u == 0);
+            commit(bars.empty(vi % kSlots));
+            if (more) {
+              s_tile(1, 1, ki);
+              commit(bars.empty(ki % kSlots));
+              if (u + 2 == U) commit(bars.q_free());
+            }
+          }
+        } else {
+          for (int u = 0; ok && u < min(U, 2); ++u) {
+            const int ki = k_item(it0, u);
+            ok = all(landed(ki));
+            if (!ok) break;
+            s_tile((x0 + u) & 1, 0, ki);
+            commit(bars.empty(ki % kSlots));
+          }
+          if (ok && U <= 2) commit(bars.q_free());
+          // O of the previous segment must have been read
+          if (ok && sg > 0) ok = all(ptx::mbar_wait(bars.o_free(), (sg - 1) & 1));
+          for (int u = 0; ok && u < U; ++u) {
+            const int x = (x0 + u) & 1, vi = v_item(it0, u, U);
+            ok = all(!*abort_flag && p_ready(x) && landed(vi));
+            if (!ok) break;
+            pv_tile(x, vi, u < 2);
+            commit(bars.empty(vi % kSlots));
+            if (u + 2 < U) {
+              const int ki = k_item(it0, u + 2);
+              ok = all(landed(ki));
+              if (!ok) break;
+              s_tile(x, 0, ki);
+              commit(bars.empty(ki % kSlots));
+              if (u + 3 == U) commit(bars.q_free());
+            }
+          }
+          x0 = (x0 + U) & 1;
+        }
+        if (ok) commit(bars.seg_done());
+        it0 += 2 * U;
       }
       if (!ok && !*abort_flag) record_timeout(p.err, abort_flag);
       // everything issued has finished before TMEM is freed
-      ptx::tc_commit(bars.exit_done());
+      commit(bars.exit_done());
       if (!ptx::mbar_wait(bars.exit_done(), 0)) record_timeout(p.err, abort_flag);
     }
-  }
   } else {
     // ================================================== softmax
     ptx::reg_inc<216>();
     const int X = (warp - 4) >> 2;
-    const int quad = warp & 3;
-    const int r = quad * 32 + lane;
+    const int quad = warp & 3;            // TMEM lane quadrant of this warp
+    const int r = quad * 32 + lane;       // lane of the row tile
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t s_addr = lane_addr + X * kTile;
     const int wg_tid = threadIdx.x - 128 - 128 * X;
-    const float cs = p.scale_log2;
     bool alive = true;
-    int u0 = 0;
+    int it0 = 0, x0 = 0, ns = 0;  // items and the turn before the segment; S tiles taken
     for (int sg = 0; walk.next(p, s); ++sg) {
-      const int u1 = u0 + s.U;
-      // this row's sequence and block row; rows past the tile's are padding
-      const int rows = s.prefix ? min(p.ns, p.B - s.b * p.ns) * p.rowsT : p.rowsT;
-      const bool row_ok = r < rows;
-      const int bq = s.prefix ? s.b * p.ns + (row_ok ? r / p.rowsT : 0) : s.b;
-      const int rt = row_ok ? (s.prefix ? r % p.rowsT : r) : 0;  // row within its sequence
+      const int U = s.U;
+      // copies of the rows in the tile, and this thread's row
+      const int copies = s.prefix ? 1 : p.copies;
+      const int span = kRows / copies;  // lanes and columns of one copy
+      const int c0 = (r / span) * span;  // first column of its keys
+      const int rc = r % span;
+      int rows = p.rowsT, bq = s.b, rt = rc;
+      if (s.prefix) {  // row tile s.b + X (wide) or s.b
+        const int b0 = (s.b + (s.wide ? X : 0)) * p.ns;
+        rows = min(p.ns, p.B - b0) * p.rowsT;
+        bq = b0 + (rc < rows ? rc / p.rowsT : 0);
+        rt = rc % p.rowsT;
+      }
+      const bool row_ok = rc < rows;
+      if (!row_ok) rt = 0;
       const int i_blk = rt / p.G;
       // cache keys this row sees: [lo, lim)
       int lim = s.n;
@@ -533,91 +776,39 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
       } else if (!p.v_blk && p.causal) {
         lim = s.n - p.blk + i_blk + 1;
       }
-      if (!row_ok) lim = 0;
       // keys from here on are not seen by the block's first row
       const int fence = s.prefix || !p.causal ? 0x7fffffff : (p.v_blk ? s.n : s.n - p.blk) + 1;
-      const bool warp_rows = quad * 32 < rows;  // any row of this warp in use
-      float m_ref = -INFINITY, l = 0.f;
-      for (int u = u0 + ((u0 & 1) != X); alive && u < u1; u += 2) {
+      // any row of this warp in use (rows past the tile's are padding: their
+      // scores are left unmasked and their results unread)
+      const bool warp_rows = (quad * 32) % span < rows;
+      RowState st{-INFINITY, 0.f};
+      int done = 0;  // tiles of this segment this warpgroup has taken
+      for (int u = s.wide ? 0 : (x0 ^ X); alive && u < U; u += s.wide ? 1 : 2, ++done) {
         if (__any_sync(full_mask, *abort_flag != 0)) { alive = false; break; }
-        const int t = s.t0 + (u - u0), st = u % kStages;
-        if (!__all_sync(full_mask, ptx::mbar_wait(bars.s_full(X), (u >> 1) & 1))) {
+        if (!__all_sync(full_mask, ptx::mbar_wait(bars.s_full(X), ns & 1))) {
           record_timeout(p.err, abort_flag); alive = false; break;
         }
+        ++ns;
         ptx::tc_fence_after();
+        const int t = s.t0 + u;
         const bool blk_tile = t == s.Tc;
         const int k0 = blk_tile ? s.n : (s.first + t) * kTile;  // position of the tile's key 0
         const int nv_tile = blk_tile ? p.blk : min(kTile, s.n - k0);
         const int lo_tile = blk_tile ? 0 : max(0, s.lo - k0);
         int nv = blk_tile ? (p.causal ? i_blk + 1 : p.blk) : lim - k0;
-        nv = row_ok ? max(0, min(nv, nv_tile)) : 0;
-        const uint32_t s_addr = lane_addr + X * kTile;
-        float f = 1.f;
-        bool rescale = false;
-        uint32_t sv[2][32];
+        nv = row_ok ? max(0, min(nv, nv_tile)) : kTile;
         if (warp_rows) {
-          float mt[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ptx::tmem_ld32(s_addr + 64 * half, sv[0]);
-            ptx::tmem_ld32(s_addr + 64 * half + 32, sv[1]);
-            ptx::tmem_wait_ld();
-            if (nv < kTile || lo_tile > 0) mask_range(sv, 64 * half, lo_tile, nv);
-#pragma unroll
-            for (int cb = 0; cb < 2; ++cb)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) mt[cb] = fmaxf(mt[cb], __uint_as_float(sv[cb][j]));
-          }
-          const float ms = fmaxf(mt[0], mt[1]) * cs;
-          const bool need = ms > m_ref + kLazyThresh;
-          rescale = __any_sync(full_mask, need);
-          if (rescale) {
-            const float m_new = need ? ms : m_ref;
-            f = m_ref == -INFINITY ? 0.f : ptx::ex2(m_ref - m_new);
-            if (!need) f = 1.f;
-            m_ref = m_new;
-          }
-        }
-        if (u > 1) {
-          if (!__all_sync(full_mask, ptx::mbar_wait(bars.pv_done(X), ((u >> 1) - 1) & 1))) {
-            record_timeout(p.err, abort_flag); alive = false; break;
-          }
-          ptx::tc_fence_after();
-        }
-        if (warp_rows) {
-          const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
-          uint8_t* prow = smem + kPOff + X * kPBytes + r * 128;
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const int half = 1 - hh;
-            if (hh == 1) {
-              ptx::tmem_ld32(s_addr, sv[0]);
-              ptx::tmem_ld32(s_addr + 32, sv[1]);
-              ptx::tmem_wait_ld();
-              ptx::tc_fence_before();
-              ptx::mbar_arrive(bars.s_free(X));
-              if (nv < kTile || lo_tile > 0) mask_range(sv, 0, lo_tile, nv);
-            }
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
-              uint32_t w4[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int kk = 8 * ch + 2 * e;
-                const float p0 = ptx::ex2(fmaf(__uint_as_float(sv[kk >> 5][kk & 31]), cs, nm));
-                const float p1 =
-                    ptx::ex2(fmaf(__uint_as_float(sv[kk >> 5][(kk & 31) + 1]), cs, nm));
-                ls[e] += p0 + p1;
-                w4[e] = ptx::pack_bf16x2(p0, p1);
-              }
-              *reinterpret_cast<uint4*>(prow + half * (kRows * 128) + ((ch ^ (r & 7)) << 4)) =
-                  make_uint4(w4[0], w4[1], w4[2], w4[3]);
-            }
-          }
-          l = l * f + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
-          if (rescale && u > u0 + 1) {
-#pragma unroll
+          bool rescale;
+          float f;
+          const float sc = p.scale_log2;
+          if (copies == 1)
+            f = softmax_tile<128>(s_addr, 0, lo_tile, nv, sc, row_ok, st, rescale);
+          else if (copies == 2)
+            f = softmax_tile<64>(s_addr, c0, lo_tile, nv, sc, row_ok, st, rescale);
+          else
+            f = softmax_tile<32>(s_addr, c0, lo_tile, nv, sc, row_ok, st, rescale);
+          if (rescale && done > 0) {  // O holds this warpgroup's earlier tiles
+#pragma unroll 1
             for (int cb = 0; cb < kD / 32; ++cb) {
               uint32_t o[32];
               ptx::tmem_ld32_sync(lane_addr + kOCol + X * kD + cb * 32, o);
@@ -625,17 +816,18 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
               for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
               ptx::tmem_st32(lane_addr + kOCol + X * kD + cb * 32, o);
             }
-            ptx::tmem_wait_st();
           }
-        } else {
-          ptx::mbar_arrive(bars.s_free(X));
+          ptx::tmem_wait_st();
         }
         const int fz = blk_tile ? (p.causal ? 1 : kTile) : max(lo_tile, fence - k0);
-        if (nv_tile < kTile || lo_tile > 0 || fz < nv_tile) {
-          if (!__all_sync(full_mask, ptx::mbar_wait(bars.v_full(st), (u / kStages) & 1))) {
+        if ((nv_tile < kTile || lo_tile > 0 || fz < nv_tile) && !(s.wide && X)) {
+          // (a wide tile's V serves both warpgroups: the first prepares it, and
+          // its product is issued first)
+          const int vi = v_item(it0, u, U);
+          if (!__all_sync(full_mask, ptx::mbar_wait(bars.full(vi % kSlots), (vi / kSlots) & 1))) {
             record_timeout(p.err, abort_flag); alive = false; break;
           }
-          uint8_t* vt = smem + kRingOff + st * kStageBytes + 2 * kHalfTile;
+          uint8_t* vt = smem + kRingOff + (vi % kSlots) * kSlotBytes;
           // rows outside the keys [lo_tile, nv_tile) hold anything: zero them,
           // and the non-finite elements of rows [fz, nv_tile)
           for (int e = wg_tid; e < kTile * 8 * halves; e += 128) {
@@ -659,8 +851,8 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
               has_nf[sg % kFlagRing] = 1;
             }
           }
+          ptx::fence_proxy_async_smem();
         }
-        ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         ptx::mbar_arrive(bars.p_full(X));
       }
@@ -669,105 +861,144 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
         record_timeout(p.err, abort_flag);
         alive = false;
       }
-      // (max, sum) of the two warpgroups through P's shared memory, which no
-      // MMA reads any more; both must get here even after a time-out
-      float2* xch = reinterpret_cast<float2*>(smem + kPOff);
+      // every thread gets here even after a time-out
+      float2* xch = reinterpret_cast<float2*>(smem + kXchOff);
+      if (!s.wide) xch[X * kRows + r] = done ? make_float2(st.m, st.l) : make_float2(-INFINITY, 0.f);
+      if (!alive) *agreed = 1;  // so that all leave together
       ptx::named_bar_sync(1, 256);
-      if (X == 0 && wg_tid == 0) *agreed = *abort_flag;
-      const bool mine = X == (u0 & 1) || s.U > 1;  // this warpgroup had a tile
-      xch[X * kRows + r] = mine ? make_float2(m_ref, l) : make_float2(-INFINITY, 0.f);
-      ptx::named_bar_sync(1, 256);
-      const float2 a0 = xch[r], a1 = xch[kRows + r];
       const int nf = has_nf[sg % kFlagRing], bad = bad_page[sg % kFlagRing];
-      const int stop = *agreed;  // one answer for all, so that they leave together
+      const int stop = *agreed;
+      // m and the factors of the two accumulators for this lane; L over all copies
+      float m = st.m, L = st.l, f0 = 1.f, f1 = 0.f;
+      bool t0 = true, t1 = false;
+      if (!s.wide) {
+        m = -INFINITY;
+        for (int i = 0; i < 2 * copies; ++i)
+          m = fmaxf(m, xch[(i & 1) * kRows + (i >> 1) * span + rc].x);
+        L = 0.f;
+        // a sum may be NaN with a maximum of -inf (every visible score NaN)
+        auto part = [&](float2 a) { return a.x == -INFINITY ? a.y : a.y * ptx::ex2(a.x - m); };
+        for (int i = 0; i < 2 * copies; ++i)
+          L += part(xch[(i & 1) * kRows + (i >> 1) * span + rc]);
+        const float2 a0 = xch[r], a1 = xch[kRows + r];
+        f0 = a0.x == -INFINITY ? 0.f : ptx::ex2(a0.x - m);
+        f1 = a1.x == -INFINITY ? 0.f : ptx::ex2(a1.x - m);
+        t0 = a0.y != 0.f;  // any weight (or NaN) in that accumulator
+        t1 = a1.y != 0.f;
+      }
       ptx::named_bar_sync(1, 256);
       if (wg_tid == 0 && X == 0) has_nf[(sg + kFlagRing / 2) % kFlagRing] = 0;
       if (stop) break;
-      u0 = u1;
-      if (!alive) continue;
+      it0 += 2 * U;
+      if (!s.wide) x0 = (x0 + U) & 1;
       ptx::tc_fence_after();
-      const float m = fmaxf(a0.x, a1.x);
-      const float f0 = a0.x == -INFINITY ? 0.f : ptx::ex2(a0.x - m);
-      const float f1 = a1.x == -INFINITY ? 0.f : ptx::ex2(a1.x - m);
-      // sums may be NaN with a maximum of -inf (every visible score NaN)
-      const float L = (a0.x == -INFINITY ? a0.y : f0 * a0.y) + (a1.x == -INFINITY ? a1.y : f1 * a1.y);
-      const bool t0 = a0.y != 0.f, t1 = a1.y != 0.f;  // any weight (or NaN) in that half
-      // keys this row sees in this unit's pieces at all (none: zeros)
+      // keys this row sees at all (none: zeros)
       const bool direct = !s.prefix && s.U == s.T && s.lo == 0;
       const int seen = (p.v_blk ? 1 : 0) + max(0, lim);
-      const float inv = direct ? (seen > 0 ? 1.f / L : 0.f) : 1.f;
+      const float inv = 1.f / L;
       int slot = 0;
       if (s.prefix)
-        slot = s.g * p.Tq + s.b + c;
+        slot = s.unit + c;
       else if (!direct)
-        slot = tail_slot(p, s.b, s.g, c, sg == 0);
-      const int srows = s.prefix ? kRows : p.rowsT;
+        slot = tail_slot(p, s.b, s.g, c, s.t0 == 0);
+      const int srows = s.prefix ? 2 * kRows : p.rowsT;
+      const int prow = s.prefix ? (s.wide ? X * kRows : 0) + r : rt;
       float* po = (s.prefix ? p.o_p : p.o_t) + (int64_t)slot * srows * kD;
       __nv_bfloat16* orow =
           p.out + ((int64_t)(bq * p.blk + i_blk) * p.Hq + s.g * p.G + rt % p.G) * kD;
-#pragma unroll 1
-      for (int cb = 0; cb < kD / 64; ++cb) {
-        const int col = X * (kD / 2) + cb * 32;
-        float v[32];
-        if (warp_rows) {
-          // selects, not products: an O that no tile wrote may hold anything
-          uint32_t o[32];
-          ptx::tmem_ld32_sync(lane_addr + kOCol + col, o);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = t0 ? f0 * __uint_as_float(o[j]) : 0.f;
-          ptx::tmem_ld32_sync(lane_addr + kOCol + kD + col, o);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = t1 ? fmaf(f1, __uint_as_float(o[j]), v[j]) : v[j];
-        }
-        if (cb == kD / 64 - 1) {  // O is read: the next segment may overwrite it
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(bars.o_free());
-        }
-        if (!row_ok || bad) continue;
+      // columns [col, col + kN) of this row: v[] to the output or to the partial
+      auto put = [&](auto n, int col, float (&v)[16]) {
+        constexpr int kN = decltype(n)::value;
+        if (!row_ok || bad) return;
         if (nf) {
-          // non-finite V elements of the block's keys that this row sees
-          const int first = p.v_blk ? s.n + 1 : max(s.n - p.blk + 1, 0);
-          const int last = p.v_blk ? s.n + i_blk : lim - 1;
-          for (int key = first; key <= last; ++key) {
-            const __nv_bfloat16* vr;
-            const int tile = p.v_blk ? s.Tc : key / kTile - s.first;
-            if (tile < s.t0 || tile >= s.t0 + s.U) continue;
-            if (p.v_blk) {
-              vr = p.v_blk + ((int64_t)(s.b * p.blk + key - s.n) * p.Hkv + s.g) * kD;
-            } else {
-              const int id = p.table[(int64_t)s.b * p.max_pages + key / p.page_size];
-              vr = p.v_pages + (((int64_t)id * p.Hkv + s.g) * p.page_size + key % p.page_size) * kD;
-            }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float x = __bfloat162float(vr[col + j]);
-              if (!isfinite(x)) v[j] += x;
-            }
-          }
+          for (int j = 0; j < kN; ++j)
+            v[j] += nonfinite_sum<kD>(p, s.b, s.g, s.n, p.v_blk ? s.n + 1 : max(s.n - p.blk + 1, 0),
+                                      p.v_blk ? s.n + i_blk : lim - 1, s.first, s.Tc, s.t0,
+                                      s.t0 + s.U, col + j);
         }
         if (direct) {
 #pragma unroll
-          for (int j8 = 0; j8 < 4; ++j8) {
-            uint32_t w4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = 8 * j8 + 2 * e;
-              w4[e] = ptx::pack_bf16x2(seen > 0 ? v[j] * inv : 0.f,
-                                       seen > 0 ? v[j + 1] * inv : 0.f);
-            }
-            *reinterpret_cast<uint4*>(orow + col + 8 * j8) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          for (int j = 0; j < kN; j += 4) {
+            uint2 w;
+            w.x = seen > 0 ? ptx::pack_bf16x2(v[j] * inv, v[j + 1] * inv) : 0u;
+            w.y = seen > 0 ? ptx::pack_bf16x2(v[j + 2] * inv, v[j + 3] * inv) : 0u;
+            *reinterpret_cast<uint2*>(orow + col + j) = w;
           }
         } else {
-          const int row = s.prefix ? r : rt;
+          float4* at = reinterpret_cast<float4*>(po) + (col / 4) * srows + prow;
 #pragma unroll
-          for (int j4 = 0; j4 < 8; ++j4)
-            __stcg(reinterpret_cast<float4*>(po) + (col / 4 + j4) * srows + row,
-                   make_float4(v[4 * j4], v[4 * j4 + 1], v[4 * j4 + 2], v[4 * j4 + 3]));
+          for (int j = 0; j < kN; j += 4)
+            __stcg(at + (j / 4) * srows, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+        }
+      };
+      // 16 columns of O for this lane: both accumulators, or the wide unit's own
+      const uint32_t oa = lane_addr + kOCol + (s.wide ? X * kD : 0);
+      auto take = [&](int col, float (&v)[16]) {
+        if (!warp_rows) return;
+        // selects, not products: an O that no tile wrote may hold anything
+        uint32_t o[16];
+        ptx::tmem_ld16_sync(oa + col, o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = t0 ? f0 * __uint_as_float(o[j]) : 0.f;
+        if (s.wide) return;
+        ptx::tmem_ld16_sync(oa + kD + col, o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = t1 ? fmaf(f1, __uint_as_float(o[j]), v[j]) : v[j];
+      };
+      // wide: all columns; otherwise the warpgroup's half of them
+      const int col0 = s.wide ? 0 : X * (kD / 2), cols = s.wide ? kD : kD / 2;
+      // sum over kC copies, 16 columns at a time: the lanes exchange 16-byte
+      // chunks, then lane r holds 16 / kC columns of row rc
+      auto drain_copies = [&](auto nc) {
+        constexpr int kC = decltype(nc)::value, kN = 16 / kC;
+        float4* sum = reinterpret_cast<float4*>(smem + kSumOff) + X * 4 * kRows;
+#pragma unroll 1
+        for (int cb = 0; cb < kD / 2; cb += 16) {
+          float v[16];
+          take(col0 + cb, v);
+          if (cb + 16 == kD / 2) {
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bars.o_free());
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sum[j * kRows + r] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          ptx::named_bar_sync(2 + X, 128);
+          const int q0 = r / span;
+#pragma unroll
+          for (int j = 0; j < kN / 4; ++j) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < kC; ++q) {
+              const float4 x = sum[(q0 * (kN / 4) + j) * kRows + q * (kRows / kC) + rc];
+              a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+            }
+            v[4 * j] = a.x; v[4 * j + 1] = a.y; v[4 * j + 2] = a.z; v[4 * j + 3] = a.w;
+          }
+          put(std::integral_constant<int, kN>{}, col0 + cb + q0 * kN, v);
+          ptx::named_bar_sync(2 + X, 128);
+        }
+      };
+      if (copies == 4) {
+        drain_copies(std::integral_constant<int, 4>{});
+      } else if (copies == 2) {
+        drain_copies(std::integral_constant<int, 2>{});
+      } else {
+#pragma unroll 1
+        for (int cb = 0; cb < cols; cb += 16) {
+          float v[16];
+          take(col0 + cb, v);
+          if (cb + 16 == cols) {  // O is read: the next segment may overwrite it
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bars.o_free());
+          }
+          put(std::integral_constant<int, 16>{}, col0 + cb, v);
         }
       }
-      if (X == 0 && row_ok && !direct) {
+      if ((s.wide || X == 0) && row_ok && r < span && !direct) {
         // NaN in the maximum marks a piece whose pages were refused
-        float2* ml = (s.prefix ? p.ml_p : p.ml_t) + (int64_t)slot * srows + (s.prefix ? r : rt);
+        float2* ml = (s.prefix ? p.ml_p : p.ml_t) + (int64_t)slot * srows + prow;
         __stcg(ml, bad ? make_float2(__int_as_float(0x7fffffff), 0.f) : make_float2(m, L));
       }
     }
@@ -784,69 +1015,95 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
 // ------------------------------------------------------------------- merge
 
 // Grid (B * Hkv, groups of kMergeRows rows); one thread per (row, 8 dims).
+// The pieces' maxima and sums are fetched together, kBatch at a time, so that a
+// unit of many pieces costs few round trips to L2.
 template <int kD>
 __global__ void __launch_bounds__(kMergeRows * kD / 8)
-attn_paged_merge(const __grid_constant__ PagedParams p, int C) {
+attn_paged_merge(const __grid_constant__ PagedParams p) {
+  constexpr int kBatch = kD / 8;
+  __shared__ float2 sml[kBatch][kMergeRows];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv;
   const int rl = threadIdx.x % kMergeRows, c8 = threadIdx.x / kMergeRows;
   const int rt = blockIdx.y * kMergeRows + rl;
   const int n = p.ctx_lens[b];
-  if (n < 0 || n > p.max_ctx || rt >= p.rowsT) return;
+  const int chunk = p.head[0], base = p.head[1], before = p.head[2 + b];
+  if (n < 0 || n > p.max_ctx) return;
   const bool sh = shares(n, p.P, p.v_blk ? 0 : p.blk);
   const int T = tail_tiles(p, n);
-  const int chunk = p.head[0], base = p.head[1];
+  const bool row_ok = rt < p.rowsT;
+  const int i = row_ok ? rt / p.G : 0;
   __nv_bfloat16* out =
-      p.out + ((int64_t)(b * p.blk + rt / p.G) * p.Hq + g * p.G + rt % p.G) * kD + 8 * c8;
-  const int w0 = base + p.Hkv * p.head[2 + b] + g * T;
+      p.out + ((int64_t)(b * p.blk + i) * p.Hq + g * p.G + rt % p.G) * kD + 8 * c8;
+  const int w0 = base + p.Hkv * before + g * (T + kOverhead) + kOverhead;  // first tile
   int t_first = 0, t_last = -1, p_first = 0, p_last = -1;
   if (T > 0) {
     t_first = w0 / chunk;
     t_last = (w0 + T - 1) / chunk;
     if (!sh && t_first == t_last) return;  // written by the main kernel
   } else if (!sh) {  // no key at all
-    *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
+    if (row_ok) *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
     return;
   }
-  const int unit = g * p.Tq + b / p.ns;
-  const int rp = (b % p.ns) * p.rowsT + rt;
+  const int tile = b / p.ns;  // row tile of the prefix
+  const bool single = tile == p.Tq - 1 && (p.Tq & 1);
+  const int unit = single ? p.Hkv * (p.Tq / 2) + g : g * (p.Tq / 2) + tile / 2;
+  const int rp = (tile & 1) * kRows + (b % p.ns) * p.rowsT;  // (a single tile's index is even)
   if (sh) {
-    p_first = unit * p.Kp / chunk;
-    p_last = (unit * p.Kp + p.Kp - 1) / chunk;
+    const int first = unit * (p.Kp + kOverhead) + kOverhead;
+    p_first = first / chunk;
+    p_last = (first + p.Kp - 1) / chunk;
   }
-  auto tslot = [&](int c) {
-    return tail_slot(p, b, g, c, c > t_first || w0 == c * chunk);
+  // pieces in tile order: the prefix, then the tail
+  const int np = p_last - p_first + 1, pieces = np + t_last - t_first + 1;
+  auto slot_of = [&](int x) -> int64_t {
+    return x < np ? unit + p_first + x : tail_slot(p, b, g, t_first + x - np, x == np);
   };
   float M = -INFINITY, L = 0.f, acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
   bool bad = false;
-  // pieces in tile order: the prefix, then the tail
-  auto take = [&](float2 ml, const float4* o, int rows) {
-    if (ml.x != ml.x) { bad = true; return; }
-    if (ml.y == 0.f) return;  // no key of this row in the piece
-    const float m = fmaxf(M, ml.x);
+  for (int x0 = 0; x0 < pieces; x0 += kBatch) {
+    const int nx = min(kBatch, pieces - x0);
+    __syncthreads();
+    if (c8 < nx && row_ok) {
+      const int64_t slot = slot_of(x0 + c8);
+      sml[c8][rl] = __ldcg(x0 + c8 < np ? p.ml_p + slot * (2 * kRows) + rp + rt
+                                        : p.ml_t + slot * p.rowsT + rt);
+    }
+    __syncthreads();
+    if (!row_ok) continue;
+    float m = M;
+    for (int x = 0; x < nx; ++x) {
+      bad = bad || sml[x][rl].x != sml[x][rl].x;
+      if (sml[x][rl].y != 0.f) m = fmaxf(m, sml[x][rl].x);
+    }
     // equal maxima (both -inf among them) keep weight 1: sums may be NaN then
     const float wa = M == m ? 1.f : ptx::ex2(M - m);
-    const float wb = ml.x == m ? 1.f : ptx::ex2(ml.x - m);
-    const float4 lo = o[(2 * c8) * rows], hi = o[(2 * c8 + 1) * rows];
-    const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    L = fmaf(wa, L, wb * ml.y);
+    L *= wa;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = fmaf(wa, acc[e], wb * v[e]);
+    for (int e = 0; e < 8; ++e) acc[e] *= wa;
     M = m;
-  };
-  for (int c = p_first; c <= p_last; ++c) {
-    const int64_t at = (int64_t)(unit + c) * kRows;
-    take(__ldcg(p.ml_p + at + rp), reinterpret_cast<const float4*>(p.o_p + at * kD) + rp, kRows);
+#pragma unroll 4
+    for (int x = 0; x < nx; ++x) {
+      const float2 ml = sml[x][rl];
+      if (ml.y == 0.f) continue;  // no key of this row in the piece
+      const float wb = ml.x == M ? 1.f : ptx::ex2(ml.x - M);
+      const bool pre = x0 + x < np;
+      const int rows = pre ? 2 * kRows : p.rowsT;
+      // O chunk-major within a slot: [D/4][rows][4]
+      const float4* o = reinterpret_cast<const float4*>((pre ? p.o_p : p.o_t) +
+                                                        slot_of(x0 + x) * rows * kD) +
+                        (pre ? rp + rt : rt);
+      const float4 lo = __ldcg(o + (2 * c8) * rows), hi = __ldcg(o + (2 * c8 + 1) * rows);
+      const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      L = fmaf(wb, ml.y, L);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(wb, v[e], acc[e]);
+    }
   }
-  for (int c = t_first; c <= t_last; ++c) {
-    const int64_t at = (int64_t)tslot(c) * p.rowsT;
-    take(__ldcg(p.ml_t + at + rt), reinterpret_cast<const float4*>(p.o_t + at * kD) + rt, p.rowsT);
-  }
-  if (bad) return;
-  const int i = rt / p.G;
+  if (bad || !row_ok) return;
   const bool none = !p.v_blk && p.causal && n - p.blk + i + 1 <= 0;
   const float inv = 1.f / L;
   uint4 w;
@@ -898,7 +1155,7 @@ int sm_count(int device) {
 constexpr int kMaxCtas = 256;
 
 struct Layout {
-  int ns, Tq, Kp;
+  int ns, Tq, Tw, Kp;
   int64_t head, ml_p, o_p, ml_t, o_t, total;  // byte offsets
 };
 
@@ -907,14 +1164,15 @@ Layout layout(const orthrus_paged_attn_args& a) {
   const int rowsT = a.Hq / a.Hkv * a.blk;
   y.ns = kRows / rowsT;
   y.Tq = a.shared_prefix > 0 ? ceil_div(a.B, y.ns) : 0;
+  y.Tw = (y.Tq + 1) / 2;
   y.Kp = ceil_div(a.shared_prefix, kTile);
-  const int64_t ps = y.Tq ? (int64_t)a.Hkv * y.Tq + kMaxCtas : 0;
+  const int64_t ps = y.Tq ? (int64_t)a.Hkv * y.Tw + kMaxCtas : 0;
   const int64_t ts = a.shared_prefix > 0 ? (int64_t)a.B * a.Hkv + kMaxCtas : 2 * kMaxCtas;
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   y.head = 0;
   y.ml_p = up(4 * (2 + (int64_t)a.B));
-  y.o_p = up(y.ml_p + ps * kRows * 8);
-  y.ml_t = up(y.o_p + ps * kRows * a.D * 4);
+  y.o_p = up(y.ml_p + ps * 2 * kRows * 8);
+  y.ml_t = up(y.o_p + ps * 2 * kRows * a.D * 4);
   y.o_t = up(y.ml_t + ts * rowsT * 8);
   y.total = up(y.o_t + ts * rowsT * a.D * 4);
   return y;
@@ -983,14 +1241,15 @@ int paged_tc_launch(const orthrus_paged_attn_args& a, cudaStream_t st) {
   p.ml_t = reinterpret_cast<float2*>(ws + y.ml_t);
   p.o_t = reinterpret_cast<float*>(ws + y.o_t);
   p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = G; p.blk = a.blk; p.rowsT = G * a.blk;
-  p.ns = y.ns; p.Tq = y.Tq; p.Kp = y.Kp; p.P = a.shared_prefix;
+  p.copies = p.rowsT <= kRows / 4 ? 4 : p.rowsT <= kRows / 2 ? 2 : 1;
+  p.ns = y.ns; p.Tq = y.Tq; p.Tw = y.Tw; p.Kp = y.Kp; p.P = a.shared_prefix;
   p.page_size = a.page_size; p.pages = a.pages; p.max_pages = a.max_pages;
   p.max_ctx = a.max_ctx; p.causal = a.mask_mode == ORTHRUS_CAUSAL_VERIFY;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
 
   // no more CTAs than the most tiles there can be
-  const int64_t most = (int64_t)a.Hkv * y.Tq * y.Kp +
-                       (int64_t)a.Hkv * a.B * (ceil_div(a.max_ctx, kTile) + 1);
+  const int64_t most = (int64_t)a.Hkv * y.Tw * (y.Kp + kOverhead) +
+                       (int64_t)a.Hkv * a.B * (ceil_div(a.max_ctx, kTile) + 1 + kOverhead);
   const int64_t want = (most + kMinChunk - 1) / kMinChunk;
   int C = sms < kMaxCtas ? sms : kMaxCtas;
   if (want < C) C = (int)want;
@@ -1011,8 +1270,8 @@ int paged_tc_launch(const orthrus_paged_attn_args& a, cudaStream_t st) {
   cfg.gridDim = dim3(a.B * a.Hkv, ceil_div(p.rowsT, kMergeRows));
   cfg.blockDim = dim3(kMergeRows * a.D / 8);
   cfg.dynamicSmemBytes = 0;
-  e = a.D == 64 ? cudaLaunchKernelEx(&cfg, attn_paged_merge<64>, p, C)
-                : cudaLaunchKernelEx(&cfg, attn_paged_merge<128>, p, C);
+  e = a.D == 64 ? cudaLaunchKernelEx(&cfg, attn_paged_merge<64>, p)
+                : cudaLaunchKernelEx(&cfg, attn_paged_merge<128>, p);
   return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ECUDA;
 }
 

@@ -348,7 +348,7 @@ int check_shape(const orthrus_paged_attn_args* a) {
     return ORTHRUS_EUNSUPPORTED;
   if ((a->k_blk != nullptr) != (a->v_blk != nullptr)) return ORTHRUS_EINVAL;
   // grid limits, and 32-bit tile, row and slot numbers
-  const int64_t tiles = a->max_ctx / 64 + 2;
+  const int64_t tiles = a->max_ctx / 64 + 4;
   if (a->B > 65535 || a->Hkv > 65535 || (int64_t)a->B * a->Hkv * tiles > (1 << 30) ||
       (int64_t)a->B * a->blk * a->Hq > (1 << 30) ||
       (int64_t)a->pages * a->Hkv * a->page_size > 0x7fffffffll)

@@ -360,6 +360,13 @@ __device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, uint32_t
       ::"r"(dst_cluster), "r"(src_cta), "r"(bytes), "r"(bar_cluster)
       : "memory");
 }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok));
+  return ok != 0;
+}
 // Give registers back to, or take them from, the pool the CTA was launched
 // with; every warp of the warpgroup executes it (n a multiple of 8).
 template <int n> __device__ __forceinline__ void reg_dec() {
