@@ -33,7 +33,10 @@
 // are refined bin by bin to an exact element.  The sums are kept per warp, in
 // vocabulary order, so that the draw is found without another pass.
 #include <cooperative_groups.h>
+#include <float.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -49,11 +52,19 @@ constexpr int kList = kThreads;   // one entry a thread
 constexpr int kMaxCluster = 8;
 constexpr int kGroups = 64;       // maxima a CTA contributes to top-k's bound
 constexpr int kResidentBytes = 160 * 1024;  // row part a CTA may hold beside its tables
-// Values more than 44 T below the maximum (weight below 8e-20, 0 in fixed
-// point at every vocabulary size above 2^10) take no part.
-constexpr float kDropT = 44.f;
+// Values more than 44 T below the maximum weigh less than 8e-20, which is 0 in
+// fixed point: they take no part.  Lower values are read as 60 T below it.
+constexpr float kDropT = 44.f, kFloorT = 60.f;
+constexpr float kMaxT = 1.8446744e19f;  // 2^64: 60 T stays a float
 
 typedef unsigned long long u64;
+
+// 2^(i / 16)
+__constant__ double kRoots[16] = {
+    1.0, 1.0442737824274138403, 1.0905077326652576592, 1.1387886347566916537,
+    1.1892071150027210667, 1.2418578120734840486, 1.2968395546510096659, 1.3542555469368927283,
+    1.4142135623730950488, 1.4768261459394993114, 1.5422108254079408236, 1.6104903319492543082,
+    1.6817928305074290861, 1.7562521603732994831, 1.8340080864093424635, 1.9152065613971472939};
 
 struct FilterParams {
   const void* logits;
@@ -97,7 +108,14 @@ struct Sums {
 constexpr int kSums = sizeof(Sums) / 8;
 
 struct Shared {
-  u64 mass[kBins];
+  union {
+    u64 mass[kBins];  // histogram's masses
+    struct {          // or, while there are none:
+      u64 keys[kList];        // keys on their way to the list
+      ulonglong2 place[kList];  // entries and mass before each of the list's
+    };
+    ushort4 packed[kThreads];   // the counts of four bins
+  };
   Entry list[kList];
   uint32_t cnt[kBins];
   float gmax[kMaxCluster * kGroups], gmin[kMaxCluster * kGroups];
@@ -106,21 +124,28 @@ struct Shared {
   u64 tot_c[kMaxCluster], tot_m[kMaxCluster];
   u64 scan_a[kWarps], scan_b[kWarps];
   u64 part[kMaxCluster];
-  double tab[8];  // 2^(i/8)
+  double tab[16];  // 2^(i/16)
   uint32_t redu[2 * kWarps];
   Cut cut;
   uint32_t cut_key;
   int cut_idx;
   u64 list_mass;
   int list_n;
+  int staged;     // entries of `keys` that stage() has filled
+  int stage_at;   // their place in the first CTA's list
   float tau;
   u64 total;
 };
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 template <typename T>
-__device__ __forceinline__ float widen(T v) {
+__device__ __forceinline__ float no_nan(T v) {  // NaN counts as -inf
   const float x = to_f32(v);
-  return x != x ? -INFINITY : x;  // NaN never takes part
+  return x != x ? -INFINITY : x;
 }
 
 // Inclusive scan of (a, b) over the CTA; returns exclusive values in a0, b0.
@@ -160,22 +185,56 @@ filter_kernel(const FilterParams p) {
   const T* src = static_cast<const T*>(p.logits) + row * p.stride + lo;
   Shared* peer0 = cluster.map_shared_rank(&s, 0);
   constexpr int kV = kResident ? 16 / sizeof(T) : 1;  // elements read at a time
-  // f(x, i) for the elements [a, b) of this part (a a multiple of kV), kV at a
-  // time from first * kV on in steps of step * kV
+  // A row whose maximum is infinite, or so large that every other value lies
+  // further below it than matters, becomes 0 at the maximum and -inf elsewhere.
+  bool flat = false;
+  float flat_max = 0.f;
+  // f(x, i) for groups of kV elements x[0 .. kV) from i on of the part's elements
+  // [a, b) (a a multiple of kV), from group `first` on in steps of `step`;
+  // elements past b read as -inf, which takes part in nothing
   auto sweep = [&](int a, int b, int first, int step, auto f) {
     for (int i = a + first * kV; i < b; i += step * kV) {
+      float x[kV];
       if constexpr (kResident) {
         const uint4 v = *reinterpret_cast<const uint4*>(vals + i);
         const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
-        for (int j = 0; j < kV; ++j)
-          if (i + j < b) f(widen(e[j]), i + j);
+        for (int j = 0; j < kV; ++j) x[j] = to_f32(e[j]);
+        if (i + kV > b)
+#pragma unroll
+          for (int j = 0; j < kV; ++j)
+            if (i + j >= b) x[j] = -INFINITY;
       } else {
-        f(widen(src[i]), i);
+        x[0] = no_nan(src[i]);
+        if (flat) x[0] = x[0] == flat_max ? 0.f : -INFINITY;
       }
+      f(x, i);
     }
   };
-  auto each = [&](auto f) { sweep(0, nv, tid, kThreads, f); };
+  auto value = [&](int i) {  // one element
+    if (kResident) return to_f32(vals[i]);
+    const float x = no_nan(src[i]);
+    return !flat ? x : x == flat_max ? 0.f : -INFINITY;
+  };
+  // f(x, i) for every element
+  auto each = [&](auto f) {
+    sweep(0, nv, tid, kThreads, [&](const float (&x)[kV], int i) {
+#pragma unroll
+      for (int j = 0; j < kV; ++j) f(x[j], i + j);
+    });
+  };
+  // f(x, i) for the few elements that pass `likely`, with one branch a group
+  auto pick = [&](auto likely, auto f) {
+    sweep(0, nv, tid, kThreads, [&](const float (&x)[kV], int i) {
+      bool any = false;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) any |= likely(x[j]);
+      if (!any) return;
+#pragma unroll
+      for (int j = 0; j < kV; ++j)
+        if (likely(x[j])) f(x[j], i + j);
+    });
+  };
 
   // ---- the row's parameters
   float T_ = p.temperature ? p.temperature[row] : 1.f;
@@ -183,7 +242,7 @@ filter_kernel(const FilterParams p) {
   float top_p = p.top_p ? p.top_p[row] : 1.f;
   float min_p = p.min_p ? p.min_p[row] : 0.f;
   const float u = fminf(fmaxf(p.u[row], 0.f), 1.f);
-  const bool bad = !(T_ >= 0.f) || T_ == INFINITY;
+  const bool bad = !(T_ >= 0.f) || T_ > kMaxT;
   if (T_ == 0.f || top_p <= 0.f) k = 1;  // the largest, lowest index
   if (T_ == 0.f) T_ = 1.f;
   if (k <= 0 || k >= p.vocab) k = 0;
@@ -193,57 +252,81 @@ filter_kernel(const FilterParams p) {
   // ---- read this part of the row; maxima and minima of groups of eight threads
   float mx = -INFINITY, mn = INFINITY;
   if (kResident && p.vec) {
-#pragma unroll 4
-    for (int i = tid * kV; i < nv; i += kThreads * kV) {
-      if (i + kV <= nv) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + i));
-        *reinterpret_cast<uint4*>(vals + i) = v;
-        const T* e = reinterpret_cast<const T*>(&v);
+    const int whole = nv / kV * kV;
+#pragma unroll 5
+    for (int i = tid * kV; i < whole; i += kThreads * kV) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + i));
+      *reinterpret_cast<uint4*>(vals + i) = v;
+      const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          const float x = widen(e[j]);
-          mx = fmaxf(mx, x);
-          mn = fminf(mn, x);
-        }
-      } else {
-        for (int j = i; j < nv; ++j) {
-          vals[j] = src[j];
-          mx = fmaxf(mx, widen(src[j]));
-          mn = fminf(mn, widen(src[j]));
-        }
+      for (int j = 0; j < kV; ++j) {
+        mx = max_nan(mx, to_f32(e[j]));
+        mn = fminf(mn, to_f32(e[j]));
       }
+    }
+    if (tid < nv - whole) {
+      const T v = src[whole + tid];
+      vals[whole + tid] = v;
+      mx = max_nan(mx, to_f32(v));
+      mn = fminf(mn, to_f32(v));
     }
   } else {
     for (int i = tid; i < nv; i += kThreads) {
       const T v = src[i];
       if (kResident) vals[i] = v;
-      mx = fmaxf(mx, widen(v));
-      mn = fminf(mn, widen(v));
+      mx = kResident ? max_nan(mx, to_f32(v)) : fmaxf(mx, no_nan(v));
+      mn = fminf(mn, no_nan(v));
     }
   }
-#pragma unroll
-  for (int o = 4; o; o >>= 1) {
-    mx = fmaxf(mx, __shfl_xor_sync(full, mx, o));
-    mn = fminf(mn, __shfl_xor_sync(full, mn, o));
-  }
-  if ((tid & 7) < C) {  // lane i of the group tells CTA i
-    Shared* q = cluster.map_shared_rank(&s, tid & 7);
-    q->gmax[rank * kGroups + (tid >> 3)] = mx;
-    q->gmin[rank * kGroups + (tid >> 3)] = mn;
-  }
-  if (tid < 8) s.tab[tid] = exp2((double)tid * 0.125);
-  for (int b = tid; b < kBins; b += kThreads) s.cnt[b] = 0;
-  if (tid == 0) s.list_n = 0;
-  cluster.sync();
   const int groups = C * kGroups;  // a multiple of 64
-  for (int i = lane; i < groups; i += 32) {
-    mx = fmaxf(mx, s.gmax[i]);
-    mn = fminf(mn, s.gmin[i]);
-  }
+  // Every CTA hears of every group's maximum and minimum; mx and mn become the row's.
+  auto exchange = [&]() {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    mx = fmaxf(mx, __shfl_xor_sync(full, mx, o));
-    mn = fminf(mn, __shfl_xor_sync(full, mn, o));
+    for (int o = 4; o; o >>= 1) {
+      mx = max_nan(mx, __shfl_xor_sync(full, mx, o));
+      mn = fminf(mn, __shfl_xor_sync(full, mn, o));
+    }
+    if ((tid & 7) < C) {  // lane i of the group tells CTA i
+      Shared* q = cluster.map_shared_rank(&s, tid & 7);
+      q->gmax[rank * kGroups + (tid >> 3)] = mx;
+      q->gmin[rank * kGroups + (tid >> 3)] = mn;
+    }
+    cluster.sync();
+    for (int i = 2 * lane; i < groups; i += 64) {
+      const float2 a = *reinterpret_cast<const float2*>(s.gmax + i);
+      const float2 b = *reinterpret_cast<const float2*>(s.gmin + i);
+      mx = max_nan(mx, max_nan(a.x, a.y));
+      mn = fminf(mn, fminf(b.x, b.y));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      mx = max_nan(mx, __shfl_xor_sync(full, mx, o));
+      mn = fminf(mn, __shfl_xor_sync(full, mn, o));
+    }
+  };
+  // Rewrite the row's values and look again (rare).
+  auto rewrite = [&](auto f) {
+    cluster.sync();  // the maxima have been read
+    mx = -INFINITY;
+    mn = INFINITY;
+    for (int i = tid; i < nv; i += kThreads) {
+      const float x = f(to_f32(kResident ? vals[i] : src[i]));
+      if (kResident) vals[i] = from_f32<T>(x);
+      mx = fmaxf(mx, x);
+      mn = fminf(mn, x);
+    }
+    exchange();
+  };
+  if (tid < 16) s.tab[tid] = kRoots[tid];
+  for (int b = tid; b < kBins; b += kThreads) s.cnt[b] = 0;
+  if (tid == 0) s.list_n = s.staged = 0;
+  exchange();
+  if (mx != mx) rewrite([&](float x) { return x != x ? -INFINITY : x; });
+  const float reach = kDropT * T_;
+  if (!(mx - kFloorT * T_ < mx) && mx > -INFINITY) {
+    flat_max = mx;
+    rewrite([&](float x) { return x == flat_max ? 0.f : -INFINITY; });
+    flat = true;
   }
   if (bad || mx == -INFINITY) {  // the same answer in every CTA of the cluster
     if (rank == 0 && tid == 0) {
@@ -258,44 +341,65 @@ filter_kernel(const FilterParams p) {
   }
 
   const double unit = (double)(1ull << p.shift);
-  auto diff = [&](float x) { return x == mx ? 0.f : mx - x; };
-  const float reach = kDropT * T_;
-  auto takes_part = [&](float x) { return x > -INFINITY && diff(x) <= reach; };
-  // e^((x - M) / T) = 2^(n / 8) e^r with |r| <= ln 2 / 16: the eighth root of
-  // two from a table, the rest of the power of two through the exponent, e^r by
-  // its Taylor series to r^7 (next term 3e-16).  Only for values that take part.
-  const double inv_t = 1.0 / (double)T_, to8 = inv_t * (8 * 1.4426950408889634074);
+  auto takes_part = [&](float x) { return mx - x <= reach; };
+  // Weights in units of 2^-shift.  e^((x - M) / T) = 2^((n + r) / 16), |r| <= 1/2: the
+  // sixteenth root of two from a table, the rest of the power of two through the
+  // exponent, 2^(r / 16) by its Taylor series to r^5 (what is left out, 1.5e-13,
+  // is below the fixed point's step at most).  N at a time, stage by stage, which
+  // hides the FP64 latencies; a value below the floor weighs less than half a unit.
+  const double inv_t = 1.0 / (double)T_, to16 = inv_t * (16 * 1.4426950408889634074);
+  const double mxd = (double)mx;
+  const float floor_x = mx - kFloorT * T_;
+  auto weights = [&](auto nn, const float* x, double* w) {
+    constexpr int N = decltype(nn)::value;
+    constexpr double big = 6755399441055744.0;  // 1.5 * 2^52: rounds to an integer
+    constexpr double c1 = 0.69314718055994530942 / 16;
+    double r[N], e[N];
+    int n[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) r[j] = ((double)fmaxf(x[j], floor_x) - mxd) * to16;
+#pragma unroll
+    for (int j = 0; j < N; ++j) e[j] = r[j] + big;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      n[j] = __double2loint(e[j]);
+      r[j] -= e[j] - big;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      e[j] = fma(r[j], c1 * c1 * c1 * c1 * c1 / 120, c1 * c1 * c1 * c1 / 24);
+#pragma unroll
+    for (int j = 0; j < N; ++j) e[j] = fma(r[j], e[j], c1 * c1 * c1 / 6);
+#pragma unroll
+    for (int j = 0; j < N; ++j) e[j] = fma(r[j], e[j], c1 * c1 / 2);
+#pragma unroll
+    for (int j = 0; j < N; ++j) e[j] = fma(r[j], e[j], c1);
+#pragma unroll
+    for (int j = 0; j < N; ++j) e[j] = fma(r[j], e[j], 1.0) * s.tab[n[j] & 15];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      w[j] = __hiloint2double(__double2hiint(e[j]) + (((n[j] >> 4) + p.shift) << 20),
+                              __double2loint(e[j]));
+  };
   auto weight = [&](float x) {
-    const double y = x == mx ? 0.0 : ((double)x - (double)mx) * to8;
-    const double big = 6755399441055744.0;  // 1.5 * 2^52: rounds to an integer
-    const double shifted = y + big;
-    const int n = __double2loint(shifted);
-    const double r = (y - (shifted - big)) * (0.69314718055994530942 / 8);
-    double e = fma(r, 1.0 / 5040, 1.0 / 720);
-    e = fma(r, e, 1.0 / 120);
-    e = fma(r, e, 1.0 / 24);
-    e = fma(r, e, 1.0 / 6);
-    e = fma(r, e, 0.5);
-    e = fma(r, e, 1.0);
-    e = fma(r, e, 1.0) * s.tab[n & 7];
-    return __hiloint2double(__double2hiint(e) + ((n >> 3) << 20), __double2loint(e));
+    double w;
+    weights(std::integral_constant<int, 1>{}, &x, &w);
+    return w;
   };
   auto fixed = [&](double w) {
     const double big = 4503599627370496.0;  // 2^52: the sum's low bits are the integer
-    return (u64)(__double_as_longlong(fma(w, unit, big)) - __double_as_longlong(big));
+    return (u64)(__double_as_longlong(w + big) - __double_as_longlong(big));
   };
+  const double minp_w = (double)min_p * unit;
+  auto passes = [&](double w) { return w >= minp_w; };
   // bins of the histogram: equal steps of M - x over the values that take part
-  const float range = fminf(diff(mn), reach);
+  const float range = fminf(mx - mn, reach);
   const float step = range > 0.f ? ((float)kBins - 0.5f) / range : 0.f;
-  auto bin_of = [&](float x) {
-    const float f = diff(x) * step;
-    return f < (float)(kBins - 1) ? (int)f : f >= (float)(kBins - 1) ? kBins - 1 : 0;
-  };
+  auto bin_of = [&](float x) { return (int)fminf((mx - x) * step, (float)(kBins - 1)); };
   auto finish = [&](int idx, float x, u64 total) {
     p.idx[row] = idx;
     if (p.logprob)
-      p.logprob[row] = (float)((x == mx ? 0.0 : ((double)x - (double)mx) * inv_t) -
-                               log((double)total / unit));
+      p.logprob[row] = (float)(((double)x - (double)mx) * inv_t - log((double)total / unit));
   };
   // does the draw fall to an element (or part) of mass w behind mass w0?  At
   // u = 1 the last with any mass takes it
@@ -303,72 +407,105 @@ filter_kernel(const FilterParams p) {
     return w > 0 && !((double)w0 > draw) && ((double)(w0 + w) > draw || w0 + w == total);
   };
 
-  auto push = [&](float x, int i) {  // onto the first CTA's list
-    const int n = atomicAdd(&peer0->list_n, 1);
-    if (n < kList) peer0->list[n].key = ((u64)~key_of(x) << 32) | (uint32_t)(lo + i);
+  // Elements on their way to the first CTA's list: stage() collects them in this
+  // CTA, send() takes their places with one atomic and copies them, and tells
+  // how many the list holds in all (more than kList: it is not complete).
+  auto stage = [&](float x, int i) {
+    const int n = atomicAdd(&s.staged, 1);
+    if (n < kList) s.keys[n] = ((u64)~key_of(x) << 32) | (uint32_t)(lo + i);
+  };
+  auto send = [&]() {
+    __syncthreads();
+    const int n = s.staged;
+    if (tid == 0 && n) s.stage_at = atomicAdd(&peer0->list_n, n);
+    __syncthreads();
+    if (tid < n && n <= kList) {
+      const int at = s.stage_at + tid;
+      if (at < kList) peer0->list[at].key = s.keys[tid];
+    }
+    cluster.sync();
+    const int all = peer0->list_n;
+    cluster.sync();  // every CTA has read it
+    return all;
   };
   auto x_of = [&](u64 key) { return float_of(~(uint32_t)(key >> 32)); };
-  // Thread e's entry of the first CTA's list: how many entries and how much mass
-  // lie before it in the filters' order.
-  auto place = [&](int n, u64 key, int& before, u64& mass) {
-    before = 0;
-    mass = 0;
+  // In the first CTA: f(e, key, w, before, mass) for the entry e of the list's n,
+  // with how many entries and how much mass lie before it in the filters' order;
+  // wd(x) is its weight.  A short list gives each entry several threads.
+  auto order = [&](int n, auto wd, auto f) {
+    const int ways = n <= kThreads / 8 ? 8 : n <= kThreads / 4 ? 4 : n <= kThreads / 2 ? 2 : 1;
+    if (tid < n) s.list[tid].w = fixed(wd(x_of(s.list[tid].key)));
+    __syncthreads();
+    const int e = tid / ways;
+    const u64 key = e < n ? s.list[e].key : 0;
+    int before = 0;
+    u64 mass = 0;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) {
+    for (int j = tid % ways; j < n; j += ways) {
       const Entry o = s.list[j];
       const bool first = o.key < key;
       before += first;
       mass += first ? o.w : 0;
     }
+    for (int o = ways / 2; o; o >>= 1) {
+      before += __shfl_xor_sync(full, before, o);
+      mass += __shfl_xor_sync(full, mass, o);
+    }
+    if (e < n && tid % ways == 0) f(e, key, s.list[e].w, before, mass);
   };
 
   // ---- small top-k: a lower bound of the k-th largest, then a list
   if (k && 4 * k <= 3 * groups) {
     if (warp == 0) {
-      uint32_t key[kMaxCluster * kGroups / 32];
+      // largest bound found by halving [least, largest] of the maxima that still
+      // has k of them at or above it; a few more than k will do.  Halved as keys:
+      // a mask's lowest value then costs no more steps than any other
+      uint32_t g[kMaxCluster * kGroups / 32], a = 0xffffffffu, b = key_of(mx);
 #pragma unroll
-      for (int i = 0; i < kMaxCluster * kGroups / 32; ++i)
-        key[i] = 32 * i < groups ? key_of(s.gmax[lane + 32 * i]) : 0;
-      uint32_t tau = 0;  // largest value of its upper 20 bits with k keys at or above it
+      for (int i = 0; i < kMaxCluster * kGroups / 32; ++i) {
+        g[i] = 32 * i < groups ? key_of(s.gmax[lane + 32 * i]) : 0;
+        if (32 * i < groups) a = min(a, g[i]);
+      }
+      a = __reduce_min_sync(full, a);
 #pragma unroll 1
-      for (int bit = 31; bit >= 12; --bit) {
-        const uint32_t want = tau | (1u << bit);
+      for (int it = 0; it < 20; ++it) {
+        const uint32_t mid = a + (b - a + 1) / 2;
         int c = 0;
 #pragma unroll
-        for (int i = 0; i < kMaxCluster * kGroups / 32; ++i) c += key[i] >= want;
-        if (__reduce_add_sync(full, c) >= k) tau = want;
+        for (int i = 0; i < kMaxCluster * kGroups / 32; ++i)
+          c += __popc(__ballot_sync(full, g[i] >= mid));
+        if (c >= k) a = mid; else b = mid - 1;
+        if ((c >= k && c <= k + k / 4 + 8) || a == b) break;
       }
-      if (lane == 0) s.tau = tau > key_of(-INFINITY) ? float_of(tau) : -INFINITY;
+      if (lane == 0) s.tau = a > key_of(-INFINITY) ? float_of(a) : -INFINITY;
     }
     __syncthreads();
     const float tau = s.tau;
-    each([&](float x, int i) {
-      if (x >= tau && x > -INFINITY) push(x, i);
-    });
-    cluster.sync();
-    const int n = peer0->list_n;
-    cluster.sync();  // every CTA has read it
+    const float bound = fmaxf(tau, -FLT_MAX);
+    pick([&](float x) { return x >= bound; }, stage);
+    const int n = send();
     if (n <= kList) {
       if (rank != 0) return;
-      const bool mine = tid < n;
-      const u64 key = mine ? s.list[tid].key : ~0ull;
-      const float x = x_of(key);
-      const double wd = mine && takes_part(x) ? weight(x) : 0.0;
-      const u64 w = fixed(wd);
-      if (mine) s.list[tid].w = w;
-      __syncthreads();
-      int before;
-      u64 m0;
-      place(mine ? n : 0, key, before, m0);
       const int first_k = min(k, n);
-      if (mine && before == first_k - 1) s.total = m0 + w;
+      auto wd = [&](float x) { return takes_part(x) ? weight(x) : 0.0; };
+      order(n, wd, [&](int e, u64, u64 w, int before, u64 m0) {
+        s.place[e] = make_ulonglong2((u64)before, m0);
+        if (before == first_k - 1) s.total = m0 + w;
+      });
       __syncthreads();
-      const bool keep = mine && before < first_k &&
-                        (!use_p || (double)m0 < (double)top_p * (double)s.total) &&
-                        wd >= (double)min_p;
-      if (mine && !keep) s.list[tid].w = 0;
+      const u64 key = tid < n ? s.list[tid].key : 0;
+      const float x = x_of(key);
+      bool keep = false;
+      if (tid < n) {
+        const ulonglong2 at = s.place[tid];
+        keep = (int)at.x < first_k &&
+               (!use_p || (double)at.y < (double)top_p * (double)s.total) &&
+               passes(wd(x));
+        if (!keep) s.list[tid].w = 0;
+      }
       __syncthreads();
       if (!keep) return;
+      const u64 w = s.list[tid].w;
       u64 total = 0, w0 = 0;  // kept mass, and what of it lies before this index
 #pragma unroll 4
       for (int j = 0; j < n; ++j) {
@@ -379,13 +516,12 @@ filter_kernel(const FilterParams p) {
       if (holds(w0, w, (double)u * (double)total, total)) finish((int)(uint32_t)key, x, total);
       return;
     }
-    if (tid == 0) s.list_n = 0;
+    if (tid == 0) s.list_n = s.staged = 0;
   }
 
   const int slice = kBins / C;  // bins this CTA adds up for the cluster
-  // Sum the cluster's histograms and tell everybody the slices' totals; `guess`
-  // fills in masses (in coarser units) from the bins' middles.
-  auto merge_hist = [&](bool with_mass, bool guess) {
+  // Sum the cluster's histograms and tell everybody the slices' totals.
+  auto merge_hist = [&]() {
     cluster.sync();
     u64 c = 0, m = 0;
     for (int b = tid; b < slice; b += kThreads) {
@@ -395,11 +531,7 @@ filter_kernel(const FilterParams p) {
       for (int q = 0; q < C; ++q) {
         const Shared* o = cluster.map_shared_rank(&s, q);
         cc += o->cnt[bin];
-        if (with_mass) mm += o->mass[bin];
-      }
-      if (guess && cc) {
-        const float mid = step > 0.f ? ((float)bin + 0.5f) / step : 0.f;
-        mm = (u64)((double)cc * (double)exp2f(-mid * (float)to8 * 0.125f) * (unit / 256));
+        mm += o->mass[bin];
       }
       s.cnt[bin] = cc;  // only this CTA reads its own slice
       s.mass[bin] = mm;
@@ -459,8 +591,8 @@ filter_kernel(const FilterParams p) {
   };
   auto count_all = [&](bool with_mass) {
     each([&](float x, int) {
-      if (!takes_part(x)) return;
       const int b = bin_of(x);
+      if (!takes_part(x)) return;
       atomicAdd(&s.cnt[b], 1u);
       if (with_mass) atomicAdd(&s.mass[b], fixed(weight(x)));
     });
@@ -469,27 +601,60 @@ filter_kernel(const FilterParams p) {
   // and tells everybody the last one of the prefix that reaches the target.
   auto cut_list = [&](int n, bool by_mass, u64 above_c, u64 above_m, double target) {
     if (rank == 0) {
-      const bool mine = tid < n;
-      const u64 key = mine ? s.list[tid].key : ~0ull;
-      const u64 w = mine ? fixed(weight(x_of(key))) : 0;
-      if (mine) s.list[tid].w = w;
-      __syncthreads();
-      int before;
-      u64 m0;
-      place(mine ? n : 0, key, before, m0);
       auto more = [&](int c, u64 m) {  // does the prefix go on behind these?
         return by_mass ? (double)(above_m + m) < target : (double)(above_c + (u64)c) < target;
       };
-      if (mine && more(before, m0) && (before + 1 == n || !more(before + 1, m0 + w)))
-        for (int q = 0; q < C; ++q) {
-          Shared* o = cluster.map_shared_rank(&s, q);
-          o->cut_key = ~(uint32_t)(key >> 32);
-          o->cut_idx = (int)(uint32_t)key;
-          o->list_mass = above_m + m0 + w;
-        }
+      order(n, weight, [&](int, u64 key, u64 w, int before, u64 m0) {
+        if (more(before, m0) && (before + 1 == n || !more(before + 1, m0 + w)))
+          for (int q = 0; q < C; ++q) {
+            Shared* o = cluster.map_shared_rank(&s, q);
+            o->cut_key = ~(uint32_t)(key >> 32);
+            o->cut_idx = (int)(uint32_t)key;
+            o->list_mass = above_m + m0 + w;
+          }
+      });
     }
     cluster.sync();
   };
+
+  // Bin in which the counts' histogram, its masses guessed from the bins' middles,
+  // reaches the share top_p of the whole.  Every CTA adds up all bins, four a
+  // thread, which saves two cluster barriers over slices.
+  auto guess_bin = [&]() {
+    __syncthreads();
+    {
+      // a CTA's part has fewer than 2^16 elements when it is resident; a longer
+      // one saturates, and the guess may be off
+      const uint4 o = reinterpret_cast<const uint4*>(s.cnt)[tid];
+      auto sat = [](uint32_t c) { return (unsigned short)min(c, 65535u); };
+      s.packed[tid] = make_ushort4(sat(o.x), sat(o.y), sat(o.z), sat(o.w));
+    }
+    cluster.sync();
+    uint32_t cc[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < kMaxCluster; ++q) {  // all loads at once; C is a power of two
+      const ushort4 o = cluster.map_shared_rank(&s, q & (C - 1))->packed[tid];
+      if (q < C) { cc[0] += o.x; cc[1] += o.y; cc[2] += o.z; cc[3] += o.w; }
+    }
+    u64 mm[4], m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float mid = step > 0.f ? ((float)(4 * tid + j) + 0.5f) / step : 0.f;
+      mm[j] = (u64)((double)cc[j] * (double)exp2f(-mid * (float)to16 * 0.0625f) * (unit / 256));
+      m += mm[j];
+    }
+    u64 m0, z0, mt, zt;
+    block_scan(s, m, 0, m0, z0, mt, zt);
+    const double target = (double)top_p * (double)mt;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if ((double)m0 < target && !((double)(m0 + mm[j]) < target)) s.cut.bin = 4 * tid + j;
+      m0 += mm[j];
+    }
+    __syncthreads();
+    return s.cut.bin;
+  };
+  static_assert(kBins == 4 * kThreads, "four bins a thread");
 
   // Exact last element of a prefix that ends in bin `c.bin`, by count or mass.
   auto refine = [&](bool by_mass, Cut c, double target, bool need_mass, u64& mass_upto) {
@@ -529,7 +694,7 @@ filter_kernel(const FilterParams p) {
         atomicAdd(&s.cnt[(khi - key) >> sh], 1u);
         if (need_mass) atomicAdd(&s.mass[(khi - key) >> sh], fixed(weight(x)));
       });
-      merge_hist(true, false);
+      merge_hist();
       const Cut d = find(by_mass, above_c, above_m, target);
       khi -= (uint32_t)d.bin << sh;
       klo = max(klo, khi - min(khi, (1u << sh) - 1));
@@ -539,14 +704,14 @@ filter_kernel(const FilterParams p) {
       cluster.sync();  // the histograms may be cleared again
     }
     if (n <= kList) {
-      if (rank == 0 && tid == 0) s.list_n = 0;
+      if (tid == 0) s.list_n = s.staged = 0;
       cluster.sync();
       each([&](float x, int i) {
         if (!takes_part(x)) return;
         const uint32_t key = key_of(x);
-        if (key >= klo && key <= khi) push(x, i);
+        if (key >= klo && key <= khi) stage(x, i);
       });
-      cluster.sync();
+      send();
       cut_list(n, by_mass, above_c, above_m, target);
     } else {
       // n equal values: the prefix takes the first `need` of them by index
@@ -561,9 +726,8 @@ filter_kernel(const FilterParams p) {
       } else {
         need = (u64)target - above_c;
       }
-      auto at = [&](int i) { return widen(kResident ? vals[i] : src[i]); };
       u64 mine = 0;
-      for (int i = tid; i < nv; i += kThreads) mine += key_of(at(i)) == khi;
+      for (int i = tid; i < nv; i += kThreads) mine += key_of(value(i)) == khi;
       u64 a0, b0, tot, bt;
       block_scan(s, mine, 0, a0, b0, tot, bt);
       if (tid < C) cluster.map_shared_rank(&s, tid)->part[rank] = tot;
@@ -574,7 +738,7 @@ filter_kernel(const FilterParams p) {
         u64 seen = before;
         for (int i0 = 0; i0 < nv; i0 += kThreads) {
           const int i = i0 + tid;
-          const u64 hit = i < nv && key_of(at(i)) == khi ? 1 : 0;
+          const u64 hit = i < nv && key_of(value(i)) == khi ? 1 : 0;
           block_scan(s, hit, 0, a0, b0, tot, bt);
           if (hit && seen + a0 + 1 == need)
             for (int q = 0; q < C; ++q) {
@@ -596,20 +760,39 @@ filter_kernel(const FilterParams p) {
   // win: first bin of the three summed apart (use_p)
   const int seg = (nv + kWarps - 1) / kWarps, seg_v = (seg + 32 * kV - 1) / (32 * kV) * (32 * kV);
   const int w_lo = min(nv, warp * seg_v), w_hi = min(nv, w_lo + seg_v);
-  auto sum_row = [&](bool bins, int win, auto keep) {
+  auto sum_row = [&](auto with_bins, int win, auto keep) {
+    constexpr bool bins = decltype(with_bins)::value;
     Sums a = {};
-    sweep(w_lo, w_hi, lane, 32, [&](float x, int i) {
-      if (!takes_part(x)) return;
-      const double wd = weight(x);
-      const u64 w = fixed(wd);
-      if (bins) {
-        const int b = bin_of(x) - win;
-        a.all += w;
-        a.above += b < 0 ? w : 0;
+    const float wf = (float)win, wf3 = win + 2 >= kBins - 1 ? INFINITY : (float)(win + 3);
+    sweep(w_lo, w_hi, lane, 32, [&](const float (&x)[kV], int i) {
+      constexpr int N = kV < 4 ? kV : 4;
 #pragma unroll
-        for (int j = 0; j < 3; ++j) a.in[j] += b == j ? w : 0;
+      for (int j0 = 0; j0 < kV; j0 += N) {
+        double wd[N];
+        u64 w[N];
+        weights(std::integral_constant<int, N>{}, x + j0, wd);
+        bool window = false;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          w[j] = fixed(wd[j]);
+          if (bins) {
+            const float f = (mx - x[j0 + j]) * step;  // bin_of() before it is cut
+            a.all += w[j];
+            if (f < wf) a.above += w[j];
+            window |= !(f < wf) && f < wf3;
+          }
+          if (keep(x[j0 + j], i + j0 + j, wd[j])) a.minp += w[j];
+        }
+        if (bins && window) {  // three bins of thousands
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const int b = takes_part(x[j0 + j]) ? bin_of(x[j0 + j]) - win : -1;
+            if (b == 0) a.in[0] += w[j];
+            else if (b == 1) a.in[1] += w[j];
+            else if (b == 2) a.in[2] += w[j];
+          }
+        }
       }
-      a.minp += keep(x, i, wd) ? w : 0;
     });
     u64* f = reinterpret_cast<u64*>(&a);
 #pragma unroll
@@ -637,14 +820,13 @@ filter_kernel(const FilterParams p) {
   bool by_minp = !use_p && !k;  // min-p's set (all, if it is off) is what is kept
   bool summed = false;          // warp_sum / cta_sum hold the row's sums
   int cut_bin = 0, win = 0;
-  u64 kept_in = 0;              // mass kept in cut_bin
   if (k) {
     // a large k, or one among many equal logits: refine, then top-p of its mass
     // over a fresh histogram; the earlier cut counts
     cluster.sync();
     clear_hist(true);
     count_all(use_p);
-    merge_hist(true, false);
+    merge_hist();
     u64 all_c = 0, limit_m = 0;
     for (int q = 0; q < C; ++q) { all_c += s.tot_c[q]; limit_m += s.tot_m[q]; }
     if ((u64)k < all_c) {
@@ -660,7 +842,7 @@ filter_kernel(const FilterParams p) {
       cluster.sync();
       clear_hist(true);
       count_all(true);
-      merge_hist(true, false);
+      merge_hist();
       const double target = (double)top_p * (double)limit_m;
       const Cut cp = find(true, 0, 0, target);
       cluster.sync();
@@ -675,11 +857,11 @@ filter_kernel(const FilterParams p) {
     }
   } else if (use_p) {
     count_all(false);
-    merge_hist(false, true);
-    u64 guess_m = 0;
-    for (int q = 0; q < C; ++q) guess_m += s.tot_m[q];
-    win = find(true, 0, 0, (double)top_p * (double)guess_m).bin - 1;
-    sum_row(true, win, [&](float, int, double wd) { return wd >= (double)min_p; });
+    win = guess_bin() - 1;
+    if (min_p > 0.f)
+      sum_row(std::true_type{}, win, [&](float, int, double w) { return passes(w); });
+    else
+      sum_row(std::true_type{}, win, [](float, int, double) { return false; });
     Sums t = {};
     for (int q = 0; q < C; ++q) {
       t.all += s.cta_sum[q].all;
@@ -692,27 +874,29 @@ filter_kernel(const FilterParams p) {
     while (j < 3 && (double)(above + t.in[j]) < target) above += t.in[j++];
     if (j < 3 && (double)t.above < target) {  // the cut lies in bin win + j
       cut_bin = win + j;
-      each([&](float x, int i) {
-        if (takes_part(x) && bin_of(x) == cut_bin) push(x, i);
-      });
-      cluster.sync();
-      const int n = peer0->list_n;
-      cluster.sync();
+      // the bin's values, or a few more: M - bin / step with some slack
+      const float slack = 1e-5f * range + 4e-7f * fabsf(mx);
+      const float top = step > 0.f ? mx - (float)cut_bin / step + slack : INFINITY;
+      const float low = step > 0.f ? mx - (float)(cut_bin + 1) / step - slack : -FLT_MAX;
+      pick([&](float x) { return x <= top && x >= low; },
+           [&](float x, int i) {
+             if (takes_part(x) && bin_of(x) == cut_bin) stage(x, i);
+           });
+      const int n = send();
       if (n <= kList) {
         cut_list(n, true, 0, above, target);
         cut_key = s.cut_key;
         cut_idx = s.cut_idx;
-        kept_in = s.list_mass - above;
         summed = true;
         // min-p is the tighter filter if the last element kept fails it
-        by_minp = min_p > 0.f && !(weight(float_of(cut_key)) >= (double)min_p);
+        by_minp = min_p > 0.f && !passes(weight(float_of(cut_key)));
       }
     }
     if (!summed) {  // the guess was off, or the bin holds too many
       cluster.sync();
       clear_hist(true);
       count_all(true);
-      merge_hist(true, false);
+      merge_hist();
       const Cut cp = find(true, 0, 0, target);
       cluster.sync();
       u64 m;
@@ -729,18 +913,19 @@ filter_kernel(const FilterParams p) {
   // ---- kept mass of this warp's part, what lies before it, the total
   u64 mine = 0, before = 0, total = 0;
   if (summed && !by_minp) {
-    // bins before the cut's are kept whole; of its own bin, look at each element
-    if (kept_in) {
-      sweep(w_lo, w_hi, lane, 32, [&](float x, int i) {
-        if (takes_part(x) && bin_of(x) == cut_bin && kept(x, i)) mine += fixed(weight(x));
-      });
-#pragma unroll
-      for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(full, mine, o);
-    }
+    // bins before the cut's are kept whole; the elements of its own are the ones
+    // that were staged
     const Sums& a = s.warp_sum[warp];
-    mine += a.above + (cut_bin > win ? a.in[0] : 0) + (cut_bin > win + 1 ? a.in[1] : 0);
-    if (lane == 0) s.scan_a[warp] = mine;
+    if (lane == 0)
+      s.scan_a[warp] = a.above + (cut_bin > win ? a.in[0] : 0) + (cut_bin > win + 1 ? a.in[1] : 0);
     __syncthreads();
+    if (tid < s.staged) {
+      const u64 key = s.keys[tid];
+      const int i = (int)(uint32_t)key - lo;
+      if (kept(x_of(key), i)) atomicAdd(&s.scan_a[i / seg_v], fixed(weight(x_of(key))));
+    }
+    __syncthreads();
+    mine = s.scan_a[warp];
     u64 cta = 0;
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += s.scan_a[w];
@@ -753,9 +938,11 @@ filter_kernel(const FilterParams p) {
       total += s.part[q];
     }
   } else {
-    if (!summed)
-      sum_row(false, 0, [&](float x, int i, double wd) {
-        return wd >= (double)min_p && (by_minp || kept(x, i));
+    if (!summed && by_minp && min_p == 0.f)
+      sum_row(std::false_type{}, 0, [](float, int, double) { return true; });
+    else if (!summed)
+      sum_row(std::false_type{}, 0, [&](float x, int i, double w) {
+        return passes(w) && (by_minp || kept(x, i));
       });
     for (int w = 0; w < warp; ++w) before += s.warp_sum[w].minp;
     mine = s.warp_sum[warp].minp;
@@ -769,12 +956,9 @@ filter_kernel(const FilterParams p) {
   u64 run = before;
   for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
     const int i = i0 + lane;
-    const float x = i < w_hi ? widen(kResident ? vals[i] : src[i]) : -INFINITY;
-    u64 w = 0;
-    if (takes_part(x) && (by_minp || kept(x, i))) {
-      const double wd = weight(x);
-      w = wd >= (double)min_p ? fixed(wd) : 0;
-    }
+    const float x = i < w_hi ? value(i) : -INFINITY;
+    const double wd = weight(x);
+    const u64 w = passes(wd) && (by_minp || kept(x, i)) ? fixed(wd) : 0;
     u64 inc = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

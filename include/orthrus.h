@@ -299,7 +299,7 @@ int orthrus_vocab_sample(int32_t dtype, const void* logits, int32_t rows, int32_
  * u float in [0, 1) (clamped to [0, 1]; NaN as 0; at 1 the last kept index with
  * any weight).  T == 0 takes the largest logit, lowest index, logprob 0; with a
  * +inf logit only those have weight.  A row without any value above -inf gives
- * idx 0 and logprob NaN.  A temperature that is negative, infinite or NaN sets
+ * idx 0 and logprob NaN.  A temperature that is negative, above 2^64 or NaN sets
  * err (nullable) to ORTHRUS_EINVAL and leaves its row's outputs alone.
  * temperature, top_k, top_p and min_p are device arrays [rows], each nullable
  * (T = 1, filter off).  Weights are FP64, summed exactly in 64-bit fixed
