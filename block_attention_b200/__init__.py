@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -222,14 +223,14 @@ def lib() -> ctypes.CDLL:
         L.orthrus_lm_head_argmax_workspace.restype = sz
         L.orthrus_lm_head_argmax.argtypes = [i32, vp, i32, i32, i64, vp, i32, vp, vp, vp, vp,
                                              sz, vp]
-        L.orthrus_vocab_sample_filtered.argtypes = [c.POINTER(FilterArgs), vp]
+        L.orthrus_vocab_sample_filtered.argtypes = [vp, vp]  # FilterArgs, packed
         L.orthrus_rope_freqs.argtypes = [i32, c.c_double, c.POINTER(RopeScaling), vp, vp]
-        L.orthrus_rope.argtypes = [c.POINTER(RopeArgs), vp]
-        L.orthrus_paged_append.argtypes = [c.POINTER(AppendArgs), vp]
-        L.orthrus_paged_append_workspace.argtypes = [c.POINTER(AppendArgs)]
+        L.orthrus_rope.argtypes = [vp, vp]  # RopeArgs, packed
+        L.orthrus_paged_append.argtypes = [vp, vp]  # AppendArgs, packed
+        L.orthrus_paged_append_workspace.argtypes = [vp]
         L.orthrus_paged_append_workspace.restype = sz
-        L.orthrus_paged_attn.argtypes = [c.POINTER(PagedAttnArgs), vp]
-        L.orthrus_paged_attn_workspace.argtypes = [c.POINTER(PagedAttnArgs)]
+        L.orthrus_paged_attn.argtypes = [vp, vp]  # PagedAttnArgs, packed
+        L.orthrus_paged_attn_workspace.argtypes = [vp]
         L.orthrus_paged_attn_workspace.restype = sz
         _lib = L
     return _lib
@@ -662,26 +663,78 @@ ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_SCALINGS = {"linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 
 
-def _like(name, t, dtype, device, shape=None):
-    """Refuse a tensor of another type, device or shape (None: not given)."""
-    if t is None:
-        return
+# These operators are called once a layer and token, so their Python side is
+# kept short: arguments are packed by struct (a fraction of what filling a
+# ctypes structure costs), a tensor's checks are one expression, and the device
+# is switched only when it is not the current one.
+
+_CODES = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_double: "d",
+          ctypes.c_void_p: "P", ctypes.c_size_t: "N", ctypes.c_uint32: "I", ctypes.c_uint64: "Q"}
+
+
+def _packer(cls):
+    """struct.Struct.pack with the layout of the ctypes structure cls (native
+    alignment, padded to its end)."""
+    s = struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_) + "0P")
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_filter, _pack_rope = _packer(FilterArgs), _packer(RopeArgs)
+_pack_append, _pack_paged_attn = _packer(AppendArgs), _packer(PagedAttnArgs)
+_DT = {torch.float32: F32, torch.bfloat16: BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_i32, _f32, _f64 = torch.int32, torch.float32, torch.float64
+
+
+def _refuse(name, t, dtype, device, shape):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device (no CPU path)")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _on(device, stream):
-    """Context in which a call launches and allocates: the tensors' device, and
-    the given stream if there is one."""
+def _need(name, t, dtype, device, shape=None):
+    """Pointer of a contiguous tensor of that type, device and shape (None: any)."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device
+            or (shape is not None and t.shape != shape) or not t.is_contiguous()):
+        _refuse(name, t, dtype, device, shape)
+    return t.data_ptr()
+
+
+def _opt(name, t, dtype, device, shape=None):
+    """The same for an optional tensor: 0 if it is not given."""
+    return 0 if t is None else _need(name, t, dtype, device, shape)
+
+
+def _lead(name, t):
+    """(device, dtype code) of a call's main tensor."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device (no CPU path)")
+    code = _DT.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return dev, code
+
+
+def _elsewhere(device, stream):
+    """Context for a call that does not run on the current device and stream, else
+    None: it allocates and launches where its tensors and stream are."""
     if stream is not None:
         if stream.device != device:
             raise ValueError("the stream belongs to another device than the tensors")
         return torch.cuda.stream(stream)
-    return torch.cuda.device(device)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return None
 
 
 class _StreamWorkspace(Workspace):
@@ -705,7 +758,7 @@ class _StreamWorkspace(Workspace):
 def _stream_ws(ws, device, op):
     """Caller's workspace, else the current stream's default for this op."""
     if ws is None:
-        key = (device.index, op, torch.cuda.current_stream(device).cuda_stream)
+        key = (device.index, op, _raw_stream(device.index))
         ws = _default_ws.get(key)
         if ws is None:
             ws = _default_ws[key] = _StreamWorkspace(device)
@@ -732,15 +785,6 @@ def rope_freqs(rot, theta, *, scaling=None, factor=1.0, original_ctx=0.0, low=1.
     return f.to(device), m.value
 
 
-def _rot(inv_freq, device):
-    if inv_freq is None:
-        return 0
-    _like("inv_freq", inv_freq, torch.float64, device)
-    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous vector")
-    return 2 * inv_freq.numel()
-
-
 def rope(x, positions, inv_freq, *, layout=ROPE_HALF, mscale=1.0, inverse=False, out=None,
          stream=None):
     """Rotary embedding of x [rows, H, D] at positions int32 [rows]: the first
@@ -749,25 +793,31 @@ def rope(x, positions, inv_freq, *, layout=ROPE_HALF, mscale=1.0, inverse=False,
     may be views with any row and head strides (unit stride inside a head);
     ``out=x`` rotates in place.  ``inverse`` turns back: the gradient with
     respect to x of the call with the same arguments."""
-    if not x.is_cuda:
-        raise ValueError("tensors must be on a CUDA device (no CPU path)")
-    if x.dim() != 3 or (x.numel() and x.stride(2) != 1):
-        raise ValueError("x must be [rows, H, D] with unit stride inside a head")
+    dev, dt = _lead("x", x)
+    if x.dim() != 3:
+        raise ValueError("x must be [rows, H, D]")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return rope(x, positions, inv_freq, layout=layout, mscale=mscale, inverse=inverse,
+                        out=out)
     rows, H, D = x.shape
-    _like("positions", positions, torch.int32, x.device, (rows,))
-    _dev(positions)
-    if out is not None:
-        _like("out", out, x.dtype, x.device, x.shape)
-        if out.numel() and out.stride(2) != 1:
-            raise ValueError("out must have unit stride inside a head")
-    with _on(x.device, stream):
-        if out is None:
-            out = torch.empty(rows, H, D, dtype=x.dtype, device=x.device)
-        a = RopeArgs(_dtype(x), int(layout), rows, H, D, _rot(inv_freq, x.device),
-                     int(bool(inverse)), float(mscale), x.data_ptr(), x.stride(0), x.stride(1),
-                     out.data_ptr(), out.stride(0), out.stride(1), positions.data_ptr(),
-                     None if inv_freq is None else inv_freq.data_ptr())
-        _check("orthrus_rope", lib().orthrus_rope(ctypes.byref(a), _stream(stream)))
+    xr, xh, xd = x.stride()
+    if out is None:
+        out = torch.empty(rows, H, D, dtype=x.dtype, device=dev)
+    elif out.dtype is not x.dtype or out.device != dev or out.shape != x.shape:
+        _refuse("out", out, x.dtype, dev, x.shape)
+    yr, yh, yd = out.stride()
+    if (xd != 1 or yd != 1) and D > 1 and rows and H:
+        raise ValueError("x and out must have unit stride inside a head")
+    pos = _need("positions", positions, _i32, dev, (rows,))
+    freq = _opt("inv_freq", inv_freq, _f64, dev)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    a = _pack_rope(dt, layout, rows, H, D, rot, bool(inverse), mscale, x.data_ptr(), xr, xh,
+                   out.data_ptr(), yr, yh, pos, freq)
+    rc = lib().orthrus_rope(a, _raw_stream(dev.index))
+    if rc:
+        raise OrthrusError("orthrus_rope", rc)
     return out
 
 
@@ -784,86 +834,95 @@ def paged_append(k, v, k_pages, v_pages, page_table, ctx_lens, *, n_rows=None, r
     (q [rows, Hq, D]) and row_starts int32 [B + 1].  Rows may be strided views
     of one projection's output.  ``advance`` adds the rows taken to ctx_lens.
     Returns q_out (None without q)."""
-    if not k.is_cuda:
-        raise ValueError("tensors must be on a CUDA device (no CPU path)")
-    dev, dt = k.device, k.dtype
+    dev, dt = _lead("k", k)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return paged_append(k, v, k_pages, v_pages, page_table, ctx_lens, n_rows=n_rows,
+                                row_starts=row_starts, inv_freq=inv_freq, layout=layout,
+                                mscale=mscale, q=q, q_out=q_out, advance=advance, err=err,
+                                workspace=workspace)
+    ty = k.dtype
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, max_pages = page_table.shape
-    _like("page_table", page_table, torch.int32, dev)
-    _like("ctx_lens", ctx_lens, torch.int32, dev, (B,))
-    _like("n_rows", n_rows, torch.int32, dev, (B,))
-    _like("row_starts", row_starts, torch.int32, dev, (B + 1,))
-    _like("err", err, torch.int32, dev)
-    for name, t in (("v", v), ("k_pages", k_pages), ("v_pages", v_pages)):
-        _like(name, t, dt, dev)
-    _dev(page_table, ctx_lens, n_rows, row_starts, err, q_out)
-    block_dims = 3 if row_starts is not None else 4
-    layered = k.dim() == block_dims + 1
-    if k.dim() != block_dims + layered or v.shape != k.shape:
+    ragged = row_starts is not None
+    dims = k.dim()
+    layered = dims == (4 if ragged else 5)
+    if dims != (3 if ragged else 4) + layered or v.shape != k.shape:
         raise ValueError("k and v must be [B, blk, Hkv, D], or [rows, Hkv, D] with row_starts, "
                          "with an optional leading layer dimension")
-    if k_pages.dim() != 4 + layered or k_pages.shape != v_pages.shape \
-            or k_pages.stride() != v_pages.stride():
-        raise ValueError("k_pages and v_pages must be laid out alike, [pages, Hkv, page_size, D] "
-                         "with k's layer dimension")
+    if v.dtype is not ty or v.device != dev:
+        _refuse("v", v, ty, dev, None)
+    pools = k_pages.shape
+    if len(pools) != 4 + layered or v_pages.shape != pools:
+        raise ValueError("k_pages and v_pages must be [pages, Hkv, page_size, D], with k's layer "
+                         "dimension")
     if layered:
-        layers = k.shape[0]
-        if k_pages.shape[0] != layers or not (k_pages[:1].is_contiguous()):
-            raise ValueError("the pools must hold k's layers, each contiguous")
-        pages_stride = k_pages.stride(0)
+        layers, pages_stride = pools[0], k_pages.stride(0)
+        if k.shape[0] != layers or v_pages.stride(0) != pages_stride:
+            raise ValueError("the pools must hold k's layers, spaced alike")
+        kp = _need("k_pages", k_pages[0], ty, dev) if layers else 0
+        vp = _need("v_pages", v_pages[0], ty, dev) if layers else 0
     else:
         layers, pages_stride = 1, 0
-        if not k_pages.is_contiguous():
-            raise ValueError("the pools must be contiguous")
-    pages, Hkv, page_size, D = k_pages.shape[-4:]
-    if k.shape[-2:] != (Hkv, D):
+        kp = _need("k_pages", k_pages, ty, dev)
+        vp = _need("v_pages", v_pages, ty, dev)
+    pages, Hkv, page_size, D = pools[-4:]
+    shape = k.shape
+    if shape[-2] != Hkv or shape[-1] != D:
         raise ValueError("k and the pools disagree on Hkv or D")
+    if ragged:
+        blk, rows = 0, shape[-3]
+    else:
+        blk = shape[-3]
+        rows = B * blk
+        if shape[-4] != B:
+            raise ValueError("k and page_table disagree on B")
 
     def strides(t, name):
         """(layer, row, head) strides of t's rows."""
-        if t.numel() and t.stride(-1) != 1:
+        st = t.stride()
+        if st[-1] != 1 and D > 1 and t.numel():
             raise ValueError(f"{name} must have unit stride inside a head")
-        if row_starts is None:
-            if t.shape[-4] != B:
-                raise ValueError(f"{name} and page_table disagree on B")
-            if t.shape[-4] > 1 and t.shape[-3] > 1 and t.stride(-4) != t.shape[-3] * t.stride(-3):
+        row = st[-3]
+        if not ragged:
+            if blk == 1:
+                row = st[-4]
+            elif B > 1 and st[-4] != blk * row:
                 raise ValueError(f"{name}: the rows of consecutive blocks must be evenly spaced")
-            row = t.stride(-3) if t.shape[-3] > 1 else t.stride(-4)
-        else:
-            row = t.stride(-3)
-        return (t.stride(0) if layered else 0), row, t.stride(-2)
+        return (st[0] if layered else 0), row, st[-2]
 
     ks, vs = strides(k, "k"), strides(v, "v")
-    blk = k.shape[-3] if row_starts is None else 0
-    rows = k.shape[-3] if row_starts is not None else B * blk
-    Hq, qs = 0, (0, 0, 0)
+    Hq, qp, qo, qs = 0, 0, 0, (0, 0, 0)
     if q is not None:
-        if layered or q.dim() != block_dims or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != D:
+        qshape = q.shape
+        if layered or qshape[:-2] != shape[:-2] or qshape[-1] != D:
             raise ValueError("q must be shaped like k but for its heads, without layers")
-        _like("q", q, dt, dev)
-        Hq, qs = q.shape[-2], strides(q, "q")
-        _like("q_out", q_out, dt, dev, q.shape)
+        if q.dtype is not ty or q.device != dev:
+            _refuse("q", q, ty, dev, None)
+        Hq, qp, qs = qshape[-2], q.data_ptr(), strides(q, "q")
+        if q_out is None:
+            q_out = torch.empty(qshape, dtype=ty, device=dev)
+        qo = _need("q_out", q_out, ty, dev, qshape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    with _on(dev, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=dev)
-        a = AppendArgs(_dtype(k), layers, B, blk, rows, Hq, Hkv, D, page_size, pages, max_pages,
-                       _rot(inv_freq, dev), int(layout), int(bool(advance)), float(mscale),
-                       k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(), *ks, *vs,
-                       qs[1], qs[2], None if q is None else q_out.data_ptr(), k_pages.data_ptr(),
-                       v_pages.data_ptr(), pages_stride, page_table.data_ptr(), ctx_lens.data_ptr(),
-                       None if n_rows is None else n_rows.data_ptr(),
-                       None if row_starts is None else row_starts.data_ptr(),
-                       None if inv_freq is None else inv_freq.data_ptr(),
-                       None if err is None else err.data_ptr(), None, 0)
-        need = lib().orthrus_paged_append_workspace(ctypes.byref(a))
-        if need:
-            buf = _stream_ws(workspace, dev, "paged_append").get(need)
-            a.workspace, a.workspace_bytes = buf.data_ptr(), buf.numel()
-        _check("orthrus_paged_append", lib().orthrus_paged_append(ctypes.byref(a),
-                                                                  _stream(stream)))
+    ws = nbytes = 0
+    if advance:
+        buf = _stream_ws(workspace, dev, "paged_append").get(256)
+        ws, nbytes = buf.data_ptr(), buf.numel()
+    a = _pack_append(dt, layers, B, blk, rows, Hq, Hkv, D, page_size, pages, max_pages,
+                     0 if inv_freq is None else 2 * inv_freq.numel(), layout, bool(advance),
+                     mscale, k.data_ptr(), v.data_ptr(), qp, *ks, *vs, qs[1], qs[2], qo, kp, vp,
+                     pages_stride, _need("page_table", page_table, _i32, dev),
+                     _need("ctx_lens", ctx_lens, _i32, dev, (B,)),
+                     _opt("n_rows", n_rows, _i32, dev, (B,)),
+                     _opt("row_starts", row_starts, _i32, dev, (B + 1,)),
+                     _opt("inv_freq", inv_freq, _f64, dev), _opt("err", err, _i32, dev), ws,
+                     nbytes)
+    rc = lib().orthrus_paged_append(a, _raw_stream(dev.index))
+    if rc:
+        raise OrthrusError("orthrus_paged_append", rc)
     return q_out
 
 
@@ -878,38 +937,47 @@ def paged_block_attn(q, k_blk, v_blk, k_pages, v_pages, page_table, ctx_lens, ma
     ``shared_prefix``: keys common to the whole batch, read once through row 0
     of the table.  max_ctx bounds every ctx_lens entry (default: the table's
     reach).  Returns out [B, blk, Hq, D]."""
-    _dev(q, k_blk, v_blk, k_pages, v_pages, page_table, ctx_lens, out, err)
-    if q.dim() != 4 or k_pages.dim() != 4 or page_table.dim() != 2:
+    dev, dt = _lead("q", q)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return paged_block_attn(q, k_blk, v_blk, k_pages, v_pages, page_table, ctx_lens,
+                                    mask_mode, shared_prefix=shared_prefix, out=out, scale=scale,
+                                    max_ctx=max_ctx, err=err, workspace=workspace)
+    ty, shape, pools = q.dtype, q.shape, k_pages.shape
+    if len(shape) != 4 or len(pools) != 4 or page_table.dim() != 2:
         raise ValueError("q must be [B, blk, Hq, D], the pools [pages, Hkv, page_size, D], "
                          "page_table [B, max_pages]")
-    B, blk, Hq, D = q.shape
-    pages, Hkv, page_size, _ = k_pages.shape
-    max_pages = page_table.shape[1]
-    dev = q.device
-    _like("k_pages", k_pages, q.dtype, dev, (pages, Hkv, page_size, D))
-    _like("v_pages", v_pages, q.dtype, dev, k_pages.shape)
     if (k_blk is None) != (v_blk is None):
         raise ValueError("k_blk and v_blk go together")
-    _like("k_blk", k_blk, q.dtype, dev, (B, blk, Hkv, D))
-    _like("v_blk", v_blk, q.dtype, dev, (B, blk, Hkv, D))
-    _like("page_table", page_table, torch.int32, dev, (B, max_pages))
-    _like("ctx_lens", ctx_lens, torch.int32, dev, (B,))
-    _like("out", out, q.dtype, dev, q.shape)
-    _like("err", err, torch.int32, dev)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty_like(q)
-        a = PagedAttnArgs(_dtype(q), int(mask_mode), B, Hq, Hkv, D, blk, page_size, pages,
-                          max_pages, max_pages * page_size if max_ctx is None else int(max_ctx),
-                          int(shared_prefix), float(D ** -0.5 if scale is None else scale), ptr(q),
-                          ptr(k_blk), ptr(v_blk), ptr(k_pages), ptr(v_pages), ptr(page_table),
-                          ptr(ctx_lens), ptr(out), ptr(err), None, 0)
-        need = lib().orthrus_paged_attn_workspace(ctypes.byref(a))
-        if need:
-            buf = _stream_ws(workspace, dev, "paged_attn").get(need)
-            a.workspace, a.workspace_bytes = buf.data_ptr(), buf.numel()
-        _check("orthrus_paged_attn", lib().orthrus_paged_attn(ctypes.byref(a), _stream(stream)))
+    B, blk, Hq, D = shape
+    pages, Hkv, page_size, Dp = pools
+    if Dp != D:
+        raise ValueError("q and the pools disagree on D")
+    max_pages = page_table.shape[1]
+    block = (B, blk, Hkv, D)
+    if out is None:
+        out = torch.empty(shape, dtype=ty, device=dev)
+    if max_ctx is None:
+        max_ctx = max_pages * page_size
+    if scale is None:
+        scale = D ** -0.5
+    args = (dt, mask_mode, B, Hq, Hkv, D, blk, page_size, pages, max_pages, max_ctx,
+            shared_prefix, scale, _need("q", q, ty, dev), _opt("k_blk", k_blk, ty, dev, block),
+            _opt("v_blk", v_blk, ty, dev, block), _need("k_pages", k_pages, ty, dev),
+            _need("v_pages", v_pages, ty, dev, pools),
+            _need("page_table", page_table, _i32, dev, (B, max_pages)),
+            _need("ctx_lens", ctx_lens, _i32, dev, (B,)), _need("out", out, ty, dev, shape),
+            _opt("err", err, _i32, dev))
+    L = lib()
+    need = L.orthrus_paged_attn_workspace(_pack_paged_attn(*args, 0, 0))
+    ws = nbytes = 0
+    if need:
+        buf = _stream_ws(workspace, dev, "paged_attn").get(need)
+        ws, nbytes = buf.data_ptr(), buf.numel()
+    rc = L.orthrus_paged_attn(_pack_paged_attn(*args, ws, nbytes), _raw_stream(dev.index))
+    if rc:
+        raise OrthrusError("orthrus_paged_attn", rc)
     return out
 
 
@@ -920,36 +988,41 @@ def vocab_sample_filtered(logits, u, *, temperature=None, top_k=None, top_p=None
     orthrus.h).  Each parameter is a number for all rows or a device tensor
     [rows] (top_k int32, the others float32); None leaves it out.  ``logprob``
     float32 [rows] receives the token's log-probability among those kept."""
-    if not logits.is_cuda or logits.dim() != 2 or (logits.numel() and logits.stride(1) != 1):
-        raise ValueError("logits must be a 2-D CUDA tensor with unit column stride")
+    dev, dt = _lead("logits", logits)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return vocab_sample_filtered(logits, u, temperature=temperature, top_k=top_k,
+                                         top_p=top_p, min_p=min_p, idx=idx, logprob=logprob,
+                                         err=err)
     rows, vocab = logits.shape
-    dev = logits.device
+    row_stride, unit = logits.stride()
+    if unit != 1 and vocab > 1 and rows:
+        raise ValueError("logits must have unit column stride")
+    if rows < 2:
+        row_stride = max(row_stride, vocab)
+    shape = (rows,)
+    if idx is None:
+        idx = torch.empty(rows, dtype=_i32, device=dev)
+
+    kept = []  # tensors made here live until the launch
 
     def per_row(name, v, dtype):
         if v is None:
-            return None
-        if not torch.is_tensor(v):
-            return torch.full((rows,), v, dtype=dtype, device=dev)
-        _like(name, v, dtype, dev, (rows,))
-        return v
+            return 0
+        if not isinstance(v, torch.Tensor):
+            v = torch.full(shape, v, dtype=dtype, device=dev)
+            kept.append(v)
+        return _need(name, v, dtype, dev, shape)
 
-    _like("u", u, torch.float32, dev, (rows,))
-    _like("idx", idx, torch.int32, dev, (rows,))
-    _like("logprob", logprob, torch.float32, dev, (rows,))
-    _like("err", err, torch.int32, dev)
-    _dev(u, idx, logprob, err)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    with _on(dev, stream):
-        temperature = per_row("temperature", temperature, torch.float32)
-        top_k = per_row("top_k", top_k, torch.int32)
-        top_p = per_row("top_p", top_p, torch.float32)
-        min_p = per_row("min_p", min_p, torch.float32)
-        _dev(temperature, top_k, top_p, min_p)
-        if idx is None:
-            idx = torch.empty(rows, dtype=torch.int32, device=dev)
-        a = FilterArgs(_dtype(logits), rows, vocab, max(logits.stride(0), vocab) if rows < 2
-                       else logits.stride(0), logits.data_ptr(), ptr(u), ptr(temperature),
-                       ptr(top_k), ptr(top_p), ptr(min_p), ptr(idx), ptr(logprob), ptr(err))
-        _check("orthrus_vocab_sample_filtered",
-               lib().orthrus_vocab_sample_filtered(ctypes.byref(a), _stream(stream)))
+    a = _pack_filter(dt, rows, vocab, row_stride, logits.data_ptr(),
+                     _need("u", u, _f32, dev, shape), per_row("temperature", temperature, _f32),
+                     per_row("top_k", top_k, _i32), per_row("top_p", top_p, _f32),
+                     per_row("min_p", min_p, _f32), _need("idx", idx, _i32, dev, shape),
+                     _opt("logprob", logprob, _f32, dev, shape), _opt("err", err, _i32, dev))
+    rc = lib().orthrus_vocab_sample_filtered(a, _raw_stream(dev.index))
+    if rc:
+        raise OrthrusError("orthrus_vocab_sample_filtered", rc)
     return idx
