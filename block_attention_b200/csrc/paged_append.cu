@@ -1,14 +1,15 @@
 // paged_append.cu -- rotary positions and the rows of a paged K/V cache
 // (include/orthrus_paged.h).
 //
-// One kernel serves both entry points.  A CTA takes R consecutive rows: its
-// threads first evaluate the rows' scaled cosines and sines once for all
-// heads (FP64 angle in half turns, sincospi, rounded to FP32, in shared
-// memory) and look up each row's page, then walk the (row, head, chunk) units
-// of q, k and v.  A unit is one 16-byte chunk (two, a pair of halves, in the
-// half layout), so every element is read and written once with full sectors:
-// the path is bound by HBM for a prefill and by launch latency for a decoding
-// step.  When strides, alignment or rot do not allow 16-byte chunks the same
+// One kernel serves both entry points.  A CTA takes R consecutive rows and walks
+// their (row, head, chunk) units of q, k and v.  A unit is one 16-byte chunk (two,
+// a pair of halves, in the half layout), so every element is read and written
+// once with full sectors: the path is bound by HBM for a prefill and by launch
+// latency for a decoding step.  Each thread first requests the chunks of its
+// next kBatch units -- what keeps HBM busy is bytes in flight -- and while the
+// first of them travel the CTA evaluates the rows' scaled cosines and sines once
+// for all heads (FP64 angle in half turns, sincospi, rounded to FP32, in shared
+// memory).  When strides, alignment or rot do not allow 16-byte chunks the same
 // walk runs element by element.
 #include <math.h>
 
@@ -19,8 +20,21 @@ namespace orthrus {
 namespace {
 
 constexpr int kThreads = 256;
+// Units a thread has in flight, CTAs an SM holds (registers), and CTAs per SM
+// that a long call is cut into.  Measured on a ragged prefill of 15.5k rows
+// (q, k, v of 48 heads x 128, bf16) and on the queries of 8190 rows (fp32), in us:
+//   batch 4, 2 CTAs 117 / 66     batch 4, 4 CTAs 82 / 66     batch 2, 5 CTAs 78 / 56
+//   batch 2, 6 CTAs 72 / 57      the same with streaming stores 67 / 50
+//   batch 1, 8 CTAs, streaming 74 / 50
+// against 59 / 41 for the bytes at the measured copy rate.
+constexpr int kBatch = 2;
+constexpr int kCtasPerSm = 6;
+constexpr int kWaves = 32;
 constexpr int kMaxRows = 16;  // rows per CTA at most (shared row records)
 constexpr int kMaxHeadDim = 1024;
+// keeps units x divisor below 2^32 (one row a CTA above 1024 units, at most
+// 2^10 units a head)
+constexpr int64_t kMaxRowElems = 1 << 21;
 constexpr int kTableBytes = 16384;  // cosine / sine pairs a CTA may hold
 
 struct RowParams {
@@ -37,6 +51,10 @@ struct RowParams {
   int32_t* err;
   unsigned* ticket;
   int B, blk, rows, Hq, Hkv, D, page_size, pages, max_pages, rot, R, advance;
+  // units: of a rotated head's pairs, of a rotated head, of a V head, of a row's
+  // q and k, of a row; 2^32 / d rounded up for each divisor d
+  int turn_units, head_units, copy_units, qk_units, row_units;
+  uint32_t by_head, by_copy, by_row;
   double mscale, sign;
 };
 
@@ -103,82 +121,45 @@ __device__ __forceinline__ Row locate(const RowParams& p, int r, bool first) {
   return o;
 }
 
-// One 16-byte chunk (kV elements) or one element (kV == 1) as floats.
-template <typename T, int kV>
-__device__ __forceinline__ void load_v(const T* p, float (&v)[kV]) {
-  if constexpr (kV == 1) {
-    v[0] = to_f32(p[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 u = __ldg(reinterpret_cast<const float4*>(p));
-    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-  } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
+// u / d from d's reciprocal ceil(2^32 / d): exact while u d < 2^32 (d >= 2; the
+// host gives 0 for d = 1)
+__device__ __forceinline__ int divide(int u, uint32_t by) {
+  return by ? (int)__umulhi((uint32_t)u, by) : u;
 }
 
+// A chunk of kV elements as it lies in memory.
+template <typename T, int kV> struct Chunk { T e[kV]; };
 template <typename T, int kV>
-__device__ __forceinline__ void store_v(T* p, const float (&v)[kV]) {
-  if constexpr (kV == 1) {
-    p[0] = from_f32<T>(v[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    __nv_bfloat162 h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(h);
-  }
+__device__ __forceinline__ Chunk<T, kV> load_chunk(const T* p) {
+  Chunk<T, kV> c;
+  if constexpr (kV == 1)
+    c.e[0] = p[0];
+  else
+    *reinterpret_cast<uint4*>(&c) = __ldcs(reinterpret_cast<const uint4*>(p));
+  return c;
+}
+template <typename T, int kV>
+__device__ __forceinline__ void store_chunk(T* p, const Chunk<T, kV>& c) {
+  if constexpr (kV == 1)
+    p[0] = c.e[0];
+  else
+    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&c));
 }
 
-// Rotate or copy unit c of one head.  Units of a rotated head: rot/2 pairs in
-// groups of kV (half layout: chunk c and its partner rot/2 further on;
-// interleaved: one chunk holds kV/2 pairs, or for kV == 1 one pair), then the
-// D - rot values that pass through, in groups of kV.
-template <typename T, int kV, bool kInter>
-__device__ __forceinline__ void turn_unit(const T* src, T* dst, int c, int turn_units, int rot,
-                                          const float2* cs) {
-  if (c >= turn_units) {
-    const int e = rot + (c - turn_units) * kV;
-    float v[kV];
-    load_v<T, kV>(src + e, v);
-    store_v<T, kV>(dst + e, v);
-    return;
-  }
-  if constexpr (kInter && kV > 1) {
-    float v[kV], w[kV];
-    load_v<T, kV>(src + c * kV, v);
-#pragma unroll
-    for (int i = 0; i < kV / 2; ++i) {
-      const float2 t = cs[c * (kV / 2) + i];
-      w[2 * i] = rope_first(v[2 * i], v[2 * i + 1], t);
-      w[2 * i + 1] = rope_second(v[2 * i], v[2 * i + 1], t);
-    }
-    store_v<T, kV>(dst + c * kV, w);
-  } else {
-    const int a = kInter ? 2 * c : c * kV;
-    const int b = kInter ? 2 * c + 1 : c * kV + rot / 2;
-    float x1[kV], x2[kV], y1[kV], y2[kV];
-    load_v<T, kV>(src + a, x1);
-    load_v<T, kV>(src + b, x2);
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const float2 t = cs[c * kV + i];
-      y1[i] = rope_first(x1[i], x2[i], t);
-      y2[i] = rope_second(x1[i], x2[i], t);
-    }
-    store_v<T, kV>(dst + a, y1);
-    store_v<T, kV>(dst + b, y2);
-  }
-}
+// One unit on its way: where it goes, what was read, and its first pair in the
+// row's table (< 0: passes through).  A rotated unit of the half layout is chunk
+// a and its partner b, rot/2 further on; of the interleaved one a chunk of
+// kV/2 pairs (for kV == 1 the elements a and b of one pair).
+template <typename T, int kV>
+struct Unit {
+  T* dst;
+  Chunk<T, kV> a, b;
+  int pair;
+};
 
 template <typename T, int kV, bool kInter>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const RowParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) rows_kernel(const __grid_constant__ RowParams p) {
+  constexpr bool kOne = kInter && kV > 1;  // one chunk holds whole pairs
   extern __shared__ float2 cs[];  // [R][rot/2] scaled (cos, sin)
   __shared__ Row row[kMaxRows];
   const int layer = blockIdx.y;
@@ -187,51 +168,92 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowParams p) {
   const int half = p.rot / 2;
   if (threadIdx.x < nr) row[threadIdx.x] = locate(p, r0 + threadIdx.x, layer == 0);
   __syncthreads();
+
+  const int gap = kInter ? 1 : half;  // distance of a pair's elements
+  const int units = nr * p.row_units;
+  auto fetch = [&](int e, Unit<T, kV>& w) {
+    w.dst = nullptr;
+    if (e >= units) return;
+    const int rr = p.R == 1 ? 0 : divide(e, p.by_row);
+    int u = e - rr * p.row_units;
+    const Row& rw = row[rr];
+    const int64_t r = r0 + rr;
+    const T* src;
+    T* dst;
+    int c;
+    bool turn = false;
+    if (u < p.qk_units) {
+      const int h = divide(u, p.by_head);
+      c = u - h * p.head_units;
+      if (h < p.Hq) {
+        if (!rw.q_ok) return;
+        src = static_cast<const T*>(p.q) + r * p.q_row + h * p.q_head;
+        dst = static_cast<T*>(p.q_out) + r * p.qo_row + h * p.qo_head;
+      } else {
+        if (rw.base < 0) return;
+        const int g = h - p.Hq;
+        src = static_cast<const T*>(p.k) + layer * p.k_layer + r * p.k_row + g * p.k_head;
+        dst = static_cast<T*>(p.k_pages) + layer * p.pages_layer + rw.base +
+              (int64_t)g * p.page_size * p.D;
+      }
+      turn = c < p.turn_units;
+      c = turn ? c * (kInter && kV == 1 ? 2 : kV) : p.rot + (c - p.turn_units) * kV;
+    } else {
+      if (rw.base < 0) return;
+      u -= p.qk_units;
+      const int g = divide(u, p.by_copy);
+      c = (u - g * p.copy_units) * kV;
+      src = static_cast<const T*>(p.v) + layer * p.v_layer + r * p.v_row + g * p.v_head;
+      dst = static_cast<T*>(p.v_pages) + layer * p.pages_layer + rw.base +
+            (int64_t)g * p.page_size * p.D;
+    }
+    w.dst = dst + c;
+    w.pair = turn ? rr * half + (kInter ? c / 2 : c) : -1;
+    w.a = load_chunk<T, kV>(src + c);
+    if (!kOne && turn) w.b = load_chunk<T, kV>(src + c + gap);
+  };
+  auto finish = [&](Unit<T, kV>& w) {
+    if (!w.dst) return;
+    if (w.pair >= 0) {
+      const float2* t = cs + w.pair;
+      if constexpr (kOne) {
+#pragma unroll
+        for (int i = 0; i < kV / 2; ++i) {
+          const float x1 = to_f32(w.a.e[2 * i]), x2 = to_f32(w.a.e[2 * i + 1]);
+          w.a.e[2 * i] = from_f32<T>(rope_first(x1, x2, t[i]));
+          w.a.e[2 * i + 1] = from_f32<T>(rope_second(x1, x2, t[i]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const float x1 = to_f32(w.a.e[i]), x2 = to_f32(w.b.e[i]);
+          w.a.e[i] = from_f32<T>(rope_first(x1, x2, t[i]));
+          w.b.e[i] = from_f32<T>(rope_second(x1, x2, t[i]));
+        }
+        store_chunk<T, kV>(w.dst + gap, w.b);
+      }
+    }
+    store_chunk<T, kV>(w.dst, w.a);
+  };
+
+  Unit<T, kV> w[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) fetch(threadIdx.x + i * kThreads, w[i]);
   for (int e = threadIdx.x; e < nr * half; e += kThreads) {
-    const int rr = e / half, i = e - rr * half;
+    const int rr = p.R == 1 ? 0 : e / half, i = e - rr * half;
     // angle in half turns: the reduction to one turn is exact in sincospi
     double sn, cn;
     sincospi((double)row[rr].pos * p.inv_freq[i] * 0.31830988618379067154, &sn, &cn);
     cs[e] = make_float2((float)(p.mscale * cn), (float)(p.sign * p.mscale * sn));
   }
   __syncthreads();
-
-  const int turn_units = kInter && kV > 1 ? p.rot / kV : half / kV;
-  const int head_units = turn_units + (p.D - p.rot) / kV;  // of a rotated head
-  const int copy_units = p.D / kV;                         // of a V head
-  const int qk = (p.Hq + p.Hkv) * head_units;
-  const int per_row = qk + p.Hkv * copy_units;
-  for (int e = threadIdx.x; e < nr * per_row; e += kThreads) {
-    const int rr = e / per_row;
-    int u = e - rr * per_row;
-    const Row& rw = row[rr];
-    const int64_t r = r0 + rr;
-    if (u < qk) {
-      const int h = u / head_units, c = u - h * head_units;
-      const T* src;
-      T* dst;
-      if (h < p.Hq) {
-        if (!rw.q_ok) continue;
-        src = static_cast<const T*>(p.q) + r * p.q_row + h * p.q_head;
-        dst = static_cast<T*>(p.q_out) + r * p.qo_row + h * p.qo_head;
-      } else {
-        if (rw.base < 0) continue;
-        const int g = h - p.Hq;
-        src = static_cast<const T*>(p.k) + layer * p.k_layer + r * p.k_row + g * p.k_head;
-        dst = static_cast<T*>(p.k_pages) + layer * p.pages_layer + rw.base +
-              (int64_t)g * p.page_size * p.D;
-      }
-      turn_unit<T, kV, kInter>(src, dst, c, turn_units, p.rot, cs + rr * half);
-    } else {
-      if (rw.base < 0) continue;
-      u -= qk;
-      const int g = u / copy_units, c = u - g * copy_units;
-      float v[kV];
-      load_v<T, kV>(static_cast<const T*>(p.v) + layer * p.v_layer + r * p.v_row +
-                        g * p.v_head + c * kV, v);
-      store_v<T, kV>(static_cast<T*>(p.v_pages) + layer * p.pages_layer + rw.base +
-                         (int64_t)g * p.page_size * p.D + c * kV, v);
-    }
+  for (int e = threadIdx.x;;) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) finish(w[i]);
+    e += kBatch * kThreads;
+    if (e >= units) break;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) fetch(e + i * kThreads, w[i]);
   }
 
   if (!p.advance) return;
@@ -276,13 +298,16 @@ bool dtype_ok(int32_t t) { return t == ORTHRUS_F32 || t == ORTHRUS_BF16; }
 bool multiple(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 int status(cudaError_t e) { return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ECUDA; }
 
-// Rows per CTA: enough units for its threads, few enough that the rows still
-// spread over the SMs, within the shared table.
+// Rows per CTA: enough units for its threads, and of a long call as many as keep
+// kWaves CTAs for every SM, which spreads the start of a CTA (a row's sequence,
+// length and page are found one after the other, then its angles) over them;
+// few enough that a short call still reaches every SM, within the shared tables.
 int rows_per_cta(const RowParams& p, int vec) {
   const int64_t units = (int64_t)(p.Hq + 2 * p.Hkv) * p.D / vec;
-  int R = (int)(4 * kThreads / (units > 0 ? units : 1));
+  const int fill = (int)(kBatch * kThreads / (units > 0 ? units : 1));
   const int spread = ceil_div(p.rows, 148);
-  if (R > spread) R = spread;
+  int R = p.rows / (148 * kWaves);
+  if (R < fill) R = fill < spread ? fill : spread;
   const int table = kTableBytes / (int)((p.rot / 2 > 0 ? p.rot / 2 : 1) * sizeof(float2));
   if (R > table) R = table;
   if (R > kMaxRows) R = kMaxRows;
@@ -295,6 +320,19 @@ int run_rows(RowParams& p, int dtype, int layout, int layers, bool vec_ok, cudaS
   const int grain = layout == ORTHRUS_ROPE_INTERLEAVED ? p.rot : p.rot / 2;
   const bool vec = vec_ok && grain % w == 0 && (p.D - p.rot) % w == 0 && p.D % w == 0;
   p.R = rows_per_cta(p, vec ? w : 1);
+  const int v = vec ? w : 1;
+  p.turn_units = layout == ORTHRUS_ROPE_INTERLEAVED && vec ? p.rot / v : p.rot / 2 / v;
+  p.head_units = p.turn_units + (p.D - p.rot) / v;
+  p.copy_units = p.D / v;
+  p.qk_units = (p.Hq + p.Hkv) * p.head_units;
+  p.row_units = p.qk_units + p.Hkv * p.copy_units;
+  auto reciprocal = [](int d) {
+    return d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / (uint64_t)d) : 0u;
+  };
+  p.by_head = reciprocal(p.head_units);
+  p.by_copy = reciprocal(p.copy_units);
+  p.by_row = reciprocal(p.row_units);
+  if ((int64_t)p.R * p.row_units >= (1ll << 32) / p.row_units) p.R = 1;  // divide() by row_units
   if (dtype == ORTHRUS_F32)
     return status(vec ? launch_rows<float, 4>(p, layout, layers, st)
                       : launch_rows<float, 1>(p, layout, layers, st));
@@ -373,7 +411,7 @@ int orthrus_rope(const orthrus_rope_args* a, orthrus_stream_t stream) {
   if (a->H < 1 || a->inverse < 0 || a->inverse > 1 || a->x_row_stride < 0 ||
       a->x_head_stride < 0 || a->out_row_stride < 0 || a->out_head_stride < 0)
     return ORTHRUS_EINVAL;
-  if ((int64_t)a->H * a->D > (1 << 24)) return ORTHRUS_EUNSUPPORTED;
+  if ((int64_t)a->H * a->D > kMaxRowElems) return ORTHRUS_EUNSUPPORTED;
   if (a->rows == 0) return ORTHRUS_OK;
   const int es = a->dtype == ORTHRUS_F32 ? 4 : 2;
   if (!a->x || !a->out || !a->positions || !multiple(a->x, es) || !multiple(a->out, es))
@@ -405,7 +443,7 @@ int orthrus_paged_append(const orthrus_append_args* a, orthrus_stream_t stream) 
   if (a->layers < 1 || a->B < 0 || a->blk < 0 || a->Hkv < 1 || a->Hq < 0 || a->page_size < 1 ||
       a->pages < 1 || a->max_pages < 1 || a->advance < 0 || a->advance > 1)
     return ORTHRUS_EINVAL;
-  if (a->layers > 65535 || (int64_t)(a->Hq + 2ll * a->Hkv) * a->D > (1 << 24))
+  if (a->layers > 65535 || (int64_t)(a->Hq + 2ll * a->Hkv) * a->D > kMaxRowElems)
     return ORTHRUS_EUNSUPPORTED;
   if ((a->q != nullptr) != (a->Hq > 0) || (a->q && a->layers != 1)) return ORTHRUS_EINVAL;
   if (a->row_starts ? a->n_rows != nullptr : (int64_t)a->B * a->blk != a->rows)

@@ -76,7 +76,7 @@ int orthrus_rope_freqs(int32_t rot, double theta, const orthrus_rope_scaling* sc
 typedef struct orthrus_rope_args {
   int32_t dtype;
   int32_t layout;      /* orthrus_rope_layout */
-  int32_t rows, H, D;  /* rows >= 0 (0: no-op), D <= 1024 */
+  int32_t rows, H, D;  /* rows >= 0 (0: no-op), D <= 1024, H * D <= 2^21 */
   int32_t rot;         /* even, 0 <= rot <= D */
   int32_t inverse;     /* 0 or 1 */
   double mscale;       /* finite */
@@ -124,7 +124,7 @@ typedef struct orthrus_append_args {
   int32_t B;           /* sequences, >= 0 */
   int32_t blk;         /* rows of a block (row_starts NULL), >= 0 */
   int32_t rows;        /* rows of k, v and q in one layer (0: no-op) */
-  int32_t Hq, Hkv, D;  /* Hq is 0 without q; D <= 1024 */
+  int32_t Hq, Hkv, D;  /* Hq is 0 without q; D <= 1024, (Hq + 2 Hkv) * D <= 2^21 */
   int32_t page_size, pages, max_pages; /* each >= 1 */
   int32_t rot, layout; /* rot 0: no rotation */
   int32_t advance;
