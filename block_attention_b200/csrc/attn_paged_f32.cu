@@ -12,8 +12,9 @@
 // RPT + 4 shared-memory vectors for 16 RPT multiply-adds and the FP32 pipe, not
 // shared memory, bounds the tile products.  Q, K, V and P rows are padded by
 // four floats, which spreads the vectors of a column group over all banks.
-// K of the next tile loads (cp.async) while the softmax and the product with V
-// run, V of the next tile while its scores are taken.
+// P takes K's place once the scores are taken, so that two CTAs of up to 64 rows
+// share an SM and one's loads (cp.async; each key's row is looked up once, a
+// tile ahead) hide behind the other's products.
 //
 // Row invariance.  Tiles and splits are cut by absolute key position, a
 // row's keys are taken in the same order whatever the block, and a masked key
@@ -47,19 +48,26 @@ struct F32Params {
   float scale_log2;
 };
 
+// floats of Q, of K or the P that replaces it, of V
+template <int D, int RPT>
+constexpr int kp_floats() {
+  return kKeys * (D + 4) > 16 * RPT * (kKeys + 4) ? kKeys * (D + 4) : 16 * RPT * (kKeys + 4);
+}
 template <int D, int RPT>
 constexpr int smem_floats() {
-  return 16 * RPT * (D + 4) + 2 * kKeys * (D + 4) + 16 * RPT * (kKeys + 4);
+  return 16 * RPT * (D + 4) + kp_floats<D, RPT>() + kKeys * (D + 4);
 }
 
 template <int D, int RPT>
-__global__ void __launch_bounds__(kThreads) f32_kernel(const F32Params p) {
+__global__ void __launch_bounds__(kThreads, RPT < 8 ? 2 : 1) f32_kernel(const F32Params p) {
   constexpr int kLd = D + 4, kPLd = kKeys + 4, kDims = D / 16;  // dims of a thread
   extern __shared__ float sm[];
+  __shared__ int64_t where[2][kKeys];  // element offset of each key's row in its tensor
+  __shared__ int8_t from[2][kKeys];    // 0: nothing (zero), 1: the pools, 2: the block rows
   float* Qs = sm;
   float* Ks = Qs + 16 * RPT * kLd;
-  float* Vs = Ks + kKeys * kLd;
-  float* Ps = Vs + kKeys * kLd;
+  float* Ps = Ks;
+  float* Vs = Ks + kp_floats<D, RPT>();
   const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int n = p.ctx_lens[b];
@@ -79,30 +87,40 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const F32Params p) {
       v = load4(p.q + ((int64_t)(b * p.blk + r / p.G) * p.Hq + g * p.G + r % p.G) * D + c);
     *reinterpret_cast<float4*>(Qs + r * kLd + c) = v;
   }
-  // one 64-key tile of K or V; keys past the range are zero-filled
-  auto issue = [&](int k0, bool is_v) {
+  // where the keys of the tile at k0 lie; those past the range are zero-filled
+  auto look_up = [&](int k0, int buf) {
+    if (tid >= kKeys) return;
+    const int pos = k0 + tid;
+    int kind = 0;
+    int64_t at = 0;
+    if (pos < min(n, hi)) {
+      const int row = shared && pos < p.P ? 0 : b;
+      const int id = p.table[(int64_t)row * p.max_pages + pos / p.page_size];
+      if (id >= 0 && id < p.pages) {
+        kind = 1;
+        at = (((int64_t)id * p.Hkv + g) * p.page_size + pos % p.page_size) * D;
+      } else {
+        bad = true;
+      }
+    } else if (pos >= n && pos < hi) {
+      kind = 2;
+      at = ((int64_t)(b * p.blk + pos - n) * p.Hkv + g) * D;
+    }
+    where[buf][tid] = at;
+    from[buf][tid] = (int8_t)kind;
+  };
+  auto issue = [&](int buf, bool is_v) {
     const float* pool = is_v ? p.v_pages : p.k_pages;
     const float* blk = is_v ? p.v_blk : p.k_blk;
     float* dst = is_v ? Vs : Ks;
-    for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
+#pragma unroll
+    for (int it = 0; it < kKeys * (D / 4) / kThreads; ++it) {
+      const int e = tid + it * kThreads;
       const int j = e / (D / 4), c = e % (D / 4) * 4;
-      const int pos = k0 + j;
-      const float* src = pool;
-      uint32_t bytes = 0;
-      if (pos < min(n, hi)) {
-        const int row = shared && pos < p.P ? 0 : b;
-        const int id = p.table[(int64_t)row * p.max_pages + pos / p.page_size];
-        if (id >= 0 && id < p.pages) {
-          src = pool + (((int64_t)id * p.Hkv + g) * p.page_size + pos % p.page_size) * D + c;
-          bytes = 16;
-        } else {
-          bad = true;
-        }
-      } else if (pos >= n && pos < hi) {
-        src = blk + ((int64_t)(b * p.blk + pos - n) * p.Hkv + g) * D + c;
-        bytes = 16;
-      }
-      ptx::cp_async16_zfill(ptx::smem_u32(dst + j * kLd + c), src, bytes);
+      const int kind = from[buf][j];
+      const float* src = kind == 2 ? blk : pool;
+      ptx::cp_async16_zfill(ptx::smem_u32(dst + j * kLd + c), src + where[buf][j] + c,
+                            kind ? 16 : 0);
     }
     ptx::cp_async_commit();
   };
@@ -120,11 +138,16 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const F32Params p) {
   }
   const int zone = p.causal ? total - p.blk + 1 : total;  // from here on not every row sees
   if (lo < hi) {
-    issue(lo, false);
-    issue(lo, true);
+    look_up(lo, 0);
+    __syncthreads();
+    issue(0, false);
+    issue(0, true);
   }
-  for (int k0 = lo; k0 < hi; k0 += kKeys) {
-    ptx::cp_async_wait<1>();  // K(k0), or everything older than the last group
+  int buf = 0;
+  for (int k0 = lo; k0 < hi; k0 += kKeys, buf ^= 1) {
+    const bool more = k0 + kKeys < hi;
+    if (more) look_up(k0 + kKeys, buf ^ 1);
+    ptx::cp_async_wait<1>();  // K
     __syncthreads();
     // ---- scores: rows ty*RPT.., keys tx + 16 j (a column group's key rows
     // lie 16 apart, so that their vectors fall into different banks)
@@ -151,9 +174,7 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const F32Params p) {
         }
       }
     }
-    __syncthreads();  // K is read
-    const bool more = k0 + kKeys < hi;
-    if (more) issue(k0 + kKeys, false);
+    __syncthreads();  // K is read: P may replace it
     // ---- softmax of the tile, row by row over the 16 threads of a row group
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
@@ -183,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const F32Params p) {
 #pragma unroll
       for (int d = 0; d < kDims; ++d) o[i][d] *= f;
     }
-    if (more) ptx::cp_async_wait<1>(); else ptx::cp_async_wait<0>();  // V(k0)
+    ptx::cp_async_wait<0>();  // V
     __syncthreads();
     // ---- O += P V: dims 4 tx + 64 d + (0..3)
     const int keys = min(kKeys, hi - k0);
@@ -225,7 +246,10 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const F32Params p) {
       }
     }
     __syncthreads();  // V and P are read
-    if (more) issue(k0 + kKeys, true);
+    if (more) {
+      issue(buf ^ 1, false);
+      issue(buf ^ 1, true);
+    }
   }
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) set_err(p.err, ORTHRUS_EINVAL);
@@ -251,7 +275,8 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const F32Params p) {
   }
 }
 
-// One warp per query row, D/32 dims a lane; splits in index order.
+// One warp per query row, D/32 dims a lane; splits in index order, the maxima and
+// sums of 32 of them fetched at once.
 template <int D>
 __global__ void __launch_bounds__(128) f32_merge(const F32Params p) {
   const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -266,17 +291,32 @@ __global__ void __launch_bounds__(128) f32_merge(const F32Params p) {
   bool bad = false;
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) acc[d] = 0.f;
-  for (int s = 0; s < S; ++s) {
-    const float2 ml = p.ml[at + (int64_t)s * p.rows];
-    if (ml.x != ml.x) bad = true;
-    if (ml.y == 0.f) continue;  // the row sees no key of this split
-    const float m = fmaxf(M, ml.x);
-    const float wa = M == m ? 1.f : exp2f(M - m), wb = ml.x == m ? 1.f : exp2f(ml.x - m);
-    L = fmaf(wa, L, __fmul_rn(wb, ml.y));
+  for (int s0 = 0; s0 < S; s0 += 32) {
+    const int ns = min(32, S - s0);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < ns) ml = p.ml[at + (int64_t)(s0 + lane) * p.rows];
+    bad = bad || __any_sync(0xffffffffu, ml.x != ml.x);
+    // the row sees no key of a split whose sum is 0
+    float m = ml.y != 0.f ? ml.x : -INFINITY;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-      acc[d] = fmaf(wa, acc[d], __fmul_rn(wb, p.o[(at + (int64_t)s * p.rows) * D + lane + 32 * d]));
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = fmaxf(M, m);
+    const float wa = M == m ? 1.f : exp2f(M - m);
+    const float wl = ml.y == 0.f ? 0.f : ml.x == m ? 1.f : exp2f(ml.x - m);
+    const unsigned used = __ballot_sync(0xffffffffu, ml.y != 0.f);
+    L *= wa;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) acc[d] *= wa;
     M = m;
+#pragma unroll 4
+    for (int s = 0; s < ns; ++s) {
+      if (!(used >> s & 1)) continue;  // warp-uniform
+      const float w = __shfl_sync(0xffffffffu, wl, s);
+      L = fmaf(w, __shfl_sync(0xffffffffu, ml.y, s), L);
+      const float* o = p.o + (at + (int64_t)(s0 + s) * p.rows) * D + lane;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(w, o[32 * d], acc[d]);
+    }
   }
   if (bad) return;
   const int i = r / p.G;
