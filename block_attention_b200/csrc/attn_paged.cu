@@ -76,6 +76,7 @@ constexpr int kFlagRing = 8;        // segments whose flags may be alive at once
 constexpr int kOverhead = 2;        // a unit's start and end, in tiles
 constexpr int kMinChunk = 4;        // tiles and overheads a CTA takes at least
 constexpr int kMergeRows = 8;       // query rows of one merging CTA
+constexpr int kMergeWays = 4, kMergeDepth = 5;  // (attn_paged_merge)
 
 constexpr int kHalfTile = kTile * 128;      // one 64-dim half of a K or V tile (16 KB)
 constexpr int kSlotBytes = 2 * kHalfTile;
@@ -1014,18 +1015,23 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
 
 // ------------------------------------------------------------------- merge
 
-// Grid (B * Hkv, groups of kMergeRows rows); one thread per (row, 8 dims).
-// The pieces' maxima and sums are fetched together, kBatch at a time, so that a
-// unit of many pieces costs few round trips to L2.
-template <int kD>
-__global__ void __launch_bounds__(kMergeRows * kD / 8)
+// Grid (B * Hkv, groups of kMergeRows rows).  A thread takes 8 dims of a row over
+// every kWays-th piece, kMergeDepth of them at a time: their maxima, sums and O are
+// requested together, so that a unit of up to kWays * kMergeDepth pieces costs one
+// round trip to L2 behind the schedule's.  The ways meet in shared memory.  Four
+// ways where units are few and their pieces many (one sequence of 8192 keys, 17
+// pieces: 26.2 us a call, one way 34.7), one otherwise (16 ragged sequences, two
+// pieces: one way 276, four 297).
+template <int kD, int kWays>
+__global__ void __launch_bounds__(kWays * kMergeRows * kD / 8)
 attn_paged_merge(const __grid_constant__ PagedParams p) {
-  constexpr int kBatch = kD / 8;
-  __shared__ float2 sml[kBatch][kMergeRows];
+  constexpr int kWay = kMergeRows * kD / 8;  // threads of one way
+  __shared__ float part[kWays > 1 ? kWays - 1 : 1][10][kWay];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  const int way = threadIdx.x / kWay, wt = threadIdx.x % kWay;
   const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv;
-  const int rl = threadIdx.x % kMergeRows, c8 = threadIdx.x / kMergeRows;
+  const int rl = wt % kMergeRows, c8 = wt / kMergeRows;
   const int rt = blockIdx.y * kMergeRows + rl;
   const int n = p.ctx_lens[b];
   const int chunk = p.head[0], base = p.head[1], before = p.head[2 + b];
@@ -1043,7 +1049,7 @@ attn_paged_merge(const __grid_constant__ PagedParams p) {
     t_last = (w0 + T - 1) / chunk;
     if (!sh && t_first == t_last) return;  // written by the main kernel
   } else if (!sh) {  // no key at all
-    if (row_ok) *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
+    if (row_ok && way == 0) *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
     return;
   }
   const int tile = b / p.ns;  // row tile of the prefix
@@ -1055,7 +1061,7 @@ attn_paged_merge(const __grid_constant__ PagedParams p) {
     p_first = first / chunk;
     p_last = (first + p.Kp - 1) / chunk;
   }
-  // pieces in tile order: the prefix, then the tail
+  // pieces: the prefix's, then the tail's
   const int np = p_last - p_first + 1, pieces = np + t_last - t_first + 1;
   auto slot_of = [&](int x) -> int64_t {
     return x < np ? unit + p_first + x : tail_slot(p, b, g, t_first + x - np, x == np);
@@ -1063,44 +1069,64 @@ attn_paged_merge(const __grid_constant__ PagedParams p) {
   float M = -INFINITY, L = 0.f, acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  bool bad = false;
-  for (int x0 = 0; x0 < pieces; x0 += kBatch) {
-    const int nx = min(kBatch, pieces - x0);
-    __syncthreads();
-    if (c8 < nx && row_ok) {
-      const int64_t slot = slot_of(x0 + c8);
-      sml[c8][rl] = __ldcg(x0 + c8 < np ? p.ml_p + slot * (2 * kRows) + rp + rt
-                                        : p.ml_t + slot * p.rowsT + rt);
-    }
-    __syncthreads();
-    if (!row_ok) continue;
-    float m = M;
-    for (int x = 0; x < nx; ++x) {
-      bad = bad || sml[x][rl].x != sml[x][rl].x;
-      if (sml[x][rl].y != 0.f) m = fmaxf(m, sml[x][rl].x);
-    }
-    // equal maxima (both -inf among them) keep weight 1: sums may be NaN then
-    const float wa = M == m ? 1.f : ptx::ex2(M - m);
-    L *= wa;
+  // another part (m, l, v) of the row: equal maxima (both -inf among them) keep
+  // weight 1, for a sum may be NaN then
+  auto add = [&](float m1, float l1, const float (&v)[8]) {
+    const float m = fmaxf(M, m1);
+    const float wa = M == m ? 1.f : ptx::ex2(M - m), wb = m1 == m ? 1.f : ptx::ex2(m1 - m);
+    L = fmaf(wa, L, wb * l1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] *= wa;
+    for (int e = 0; e < 8; ++e) acc[e] = fmaf(wa, acc[e], wb * v[e]);
     M = m;
-#pragma unroll 4
-    for (int x = 0; x < nx; ++x) {
-      const float2 ml = sml[x][rl];
-      if (ml.y == 0.f) continue;  // no key of this row in the piece
-      const float wb = ml.x == M ? 1.f : ptx::ex2(ml.x - M);
-      const bool pre = x0 + x < np;
-      const int rows = pre ? 2 * kRows : p.rowsT;
-      // O chunk-major within a slot: [D/4][rows][4]
-      const float4* o = reinterpret_cast<const float4*>((pre ? p.o_p : p.o_t) +
-                                                        slot_of(x0 + x) * rows * kD) +
-                        (pre ? rp + rt : rt);
-      const float4 lo = __ldcg(o + (2 * c8) * rows), hi = __ldcg(o + (2 * c8 + 1) * rows);
-      const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      L = fmaf(wb, ml.y, L);
+  };
+  bool bad = false;
+  if (row_ok) {
+    for (int x0 = way; x0 < pieces; x0 += kWays * kMergeDepth) {
+      float2 ml[kMergeDepth];
+      float4 o[kMergeDepth][2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(wb, v[e], acc[e]);
+      for (int j = 0; j < kMergeDepth; ++j) {
+        const int x = x0 + j * kWays;
+        ml[j] = make_float2(-INFINITY, 0.f);
+        if (x < pieces) {
+          const bool pre = x < np;
+          const int rows = pre ? 2 * kRows : p.rowsT, row = pre ? rp + rt : rt;
+          const int64_t slot = slot_of(x);
+          ml[j] = __ldcg((pre ? p.ml_p : p.ml_t) + slot * rows + row);
+          // O chunk-major within a slot: [D/4][rows][4]
+          const float4* at =
+              reinterpret_cast<const float4*>((pre ? p.o_p : p.o_t) + slot * rows * kD) + row;
+          o[j][0] = __ldcg(at + (2 * c8) * rows);
+          o[j][1] = __ldcg(at + (2 * c8 + 1) * rows);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kMergeDepth; ++j) {
+        bad = bad || ml[j].x != ml[j].x;
+        if (ml[j].y == 0.f) continue;  // no key of this row in the piece
+        const float v[8] = {o[j][0].x, o[j][0].y, o[j][0].z, o[j][0].w,
+                            o[j][1].x, o[j][1].y, o[j][1].z, o[j][1].w};
+        add(ml[j].x, ml[j].y, v);
+      }
+    }
+  }
+  if constexpr (kWays > 1) {
+    bad = __syncthreads_or(bad);  // a unit's pages are refused for all of its rows
+    if (way > 0) {
+      part[way - 1][0][wt] = M;
+      part[way - 1][1][wt] = L;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part[way - 1][2 + e][wt] = acc[e];
+    }
+    __syncthreads();
+    if (way > 0) return;
+#pragma unroll
+    for (int w = 0; w < kWays - 1; ++w) {
+      if (part[w][1][wt] == 0.f) continue;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = part[w][2 + e][wt];
+      add(part[w][0][wt], part[w][1][wt], v);
     }
   }
   if (bad || !row_ok) return;
@@ -1268,10 +1294,15 @@ int paged_tc_launch(const orthrus_paged_attn_args& a, cudaStream_t st) {
                             : cudaLaunchKernelEx(&cfg, attn_paged_kernel<128>, p);
   if (e != cudaSuccess) return ORTHRUS_ECUDA;
   cfg.gridDim = dim3(a.B * a.Hkv, ceil_div(p.rowsT, kMergeRows));
-  cfg.blockDim = dim3(kMergeRows * a.D / 8);
+  const bool many = (int64_t)a.B * a.Hkv * 4 <= C;  // pieces of a unit
+  cfg.blockDim = dim3((many ? kMergeWays : 1) * kMergeRows * a.D / 8);
   cfg.dynamicSmemBytes = 0;
-  e = a.D == 64 ? cudaLaunchKernelEx(&cfg, attn_paged_merge<64>, p)
-                : cudaLaunchKernelEx(&cfg, attn_paged_merge<128>, p);
+  if (many)
+    e = a.D == 64 ? cudaLaunchKernelEx(&cfg, attn_paged_merge<64, kMergeWays>, p)
+                  : cudaLaunchKernelEx(&cfg, attn_paged_merge<128, kMergeWays>, p);
+  else
+    e = a.D == 64 ? cudaLaunchKernelEx(&cfg, attn_paged_merge<64, 1>, p)
+                  : cudaLaunchKernelEx(&cfg, attn_paged_merge<128, 1>, p);
   return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ECUDA;
 }
 
