@@ -30,6 +30,8 @@
 //                the tiles are used (K0 K1 V0 K2 V1 ..); each lane loads one
 //                page's rows of one 64-dim half, the page ids two tiles ahead
 //   warp 1       MMA issuer (one thread)
+//   warp 2       walks the schedule ahead of the others and hands its units out
+//                through a ring in shared memory
 //   warp 3       Q tiles
 //   warps 4..11  softmax, two warpgroups X = 0, 1; a wide unit's row tile X
 //                belongs to warpgroup X, otherwise they take turns on the tiles
@@ -72,7 +74,9 @@ constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
 constexpr int kOCol = 256;
 constexpr float kLazyThresh = 8.f;  // log2 units
-constexpr int kFlagRing = 8;        // segments whose flags may be alive at once
+constexpr int kSegRing = 8;         // segments that may be alive at once
+constexpr int kFlagRing = kSegRing;
+constexpr int kSegReaders = 11;     // warps that release one: producer, Q, MMA, softmax
 constexpr int kOverhead = 2;        // a unit's start and end, in tiles
 constexpr int kMinChunk = 4;        // tiles and overheads a CTA takes at least
 constexpr int kMergeRows = 8;       // query rows of one merging CTA
@@ -86,10 +90,13 @@ constexpr int kSumOff = kXchOff + 2048;     //   row tile's space, which only wi
                                             //   (always before narrow ones) load
 constexpr int kRingOff = 2 * kQBytes;
 constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
-constexpr int kNumBars = 9 + 2 * kSlots;
-constexpr int kMiscOff = kBarOff + kNumBars * 8;
-// TMEM address, abort flag, start of the walk, scan words, segment flags
-constexpr int kSmemBytes = kMiscOff + 256 + 1024;  // + alignment slack
+constexpr int kNumBars = 9 + 2 * kSlots + 2 * kSegRing;
+constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
+// TMEM address, abort flag, start of the walk, scan words, segment flags; the
+// ring of segments
+constexpr int kSegOff = kMiscOff + 256;
+constexpr int kSegBytes = 48;
+constexpr int kSmemBytes = kSegOff + kSegRing * kSegBytes + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 static_assert(kSumOff + 2 * 4 * kRows * 16 <= kRingOff, "copy sums fit");
 
@@ -130,6 +137,8 @@ struct Bars {
   __device__ uint32_t p_full(int x) const { return at(7 + x); }  // P_X there
   __device__ uint32_t full(int s) const { return at(9 + s); }
   __device__ uint32_t empty(int s) const { return at(9 + kSlots + s); }
+  __device__ uint32_t seg_full(int s) const { return at(9 + 2 * kSlots + s); }
+  __device__ uint32_t seg_empty(int s) const { return at(9 + 2 * kSlots + kSegRing + s); }
 };
 
 __device__ __forceinline__ void record_timeout(int32_t* err, volatile int* abort_flag) {
@@ -173,9 +182,9 @@ struct Seg {
   int t0, U;   // tiles [t0, t0 + U) of the unit
   int T;       // tiles of the unit
 };
+static_assert(sizeof(Seg) == kSegBytes, "a segment is three 16-byte words");
 
-// Walks a CTA's share [pos, end) of the schedule unit by unit.  Every warp
-// role keeps one.
+// Walks a CTA's share [pos, end) of the schedule unit by unit.
 struct Walk {
   int pos, end, base;  // base: length of the prefix units
   int b, g, t;         // next position in the tails: sequence, kv-head, offset in its unit
@@ -254,21 +263,27 @@ __device__ __forceinline__ void mask32(uint32_t (&sv)[32], int k0, int lo, int h
   for (int j = 0; j < 32; ++j)
     if (k0 + j < lo || k0 + j >= hi) sv[j] = __float_as_uint(-INFINITY);
 }
-__device__ __forceinline__ float max32(const uint32_t (&sv)[32]) {
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+__device__ __forceinline__ float max32(const uint32_t (&sv)[32], float m) {
+  float a = m, b = __uint_as_float(sv[0]);
 #pragma unroll
-  for (int j = 0; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], __uint_as_float(sv[j]));
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  for (int j = 1; j < 31; j += 4) {
+    a = ptx::max3(a, __uint_as_float(sv[j]), __uint_as_float(sv[j + 1]));
+    b = ptx::max3(b, __uint_as_float(sv[j + 2]), j + 3 < 32 ? __uint_as_float(sv[j + 3]) : b);
+  }
+  return fmaxf(a, b);
 }
-// weights 2^(s c + nm) of 32 scores as bf16 pairs; adds them to ls
-__device__ __forceinline__ void exp32(const uint32_t (&sv)[32], float c, float nm, float (&ls)[4],
-                                      uint32_t* w) {
+// weights 2^(s c + nm) of 32 scores as bf16 pairs; adds them, two a time, to ls
+__device__ __forceinline__ void exp32(const uint32_t (&sv)[32], uint64_t c, uint64_t nm,
+                                      uint64_t (&ls)[2], uint32_t* w) {
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
-    const float p0 = ptx::ex2(fmaf(__uint_as_float(sv[j]), c, nm));
-    const float p1 = ptx::ex2(fmaf(__uint_as_float(sv[j + 1]), c, nm));
-    ls[(j >> 1) & 3] += p0 + p1;
-    w[j >> 1] = ptx::pack_bf16x2(p0, p1);
+    float x, y;
+    ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), c, nm),
+                 x, y);
+    x = ptx::ex2(x);
+    y = ptx::ex2(y);
+    ls[(j >> 1) & 1] = ptx::add2(ls[(j >> 1) & 1], ptx::pack2(x, y));
+    w[j >> 1] = ptx::pack_bf16x2(x, y);
   }
 }
 
@@ -297,67 +312,55 @@ __device__ __forceinline__ float raise_max(RowState& st, float ms, bool& any) {
 template <int kCols>
 __device__ __forceinline__ float softmax_tile(uint32_t s_addr, int c0, int lo, int nv, float c,
                                               bool row_ok, RowState& st, bool& rescale) {
-  float f, ls[4] = {0.f, 0.f, 0.f, 0.f};
+  constexpr int kStep = kCols < 64 ? kCols : 64;  // columns in registers at a time
+  constexpr int N = kStep / 32;
   const uint32_t p_addr = s_addr + 64;
   const bool mask = nv < c0 + kCols || lo > c0;
-  if constexpr (kCols == 128) {
-    // 64 columns at a time, so that no more scores than that are live: both
-    // halves for the maximum, the second kept into its exponentials, the first
-    // read again.  P's words 32..63 may replace S's columns 96..127 as soon as
-    // those are in registers, words 0..31 the columns 64..95.
-    uint32_t a[32], b[32], w[32];
-    ptx::tmem_ld32(s_addr, a);
-    ptx::tmem_ld32(s_addr + 32, b);
-    ptx::tmem_wait_ld();
-    if (mask) { mask32(a, 0, lo, nv); mask32(b, 32, lo, nv); }
-    float mt = fmaxf(max32(a), max32(b));
-    ptx::tmem_ld32(s_addr + 64, a);
-    ptx::tmem_ld32(s_addr + 96, b);
-    ptx::tmem_wait_ld();
-    if (mask) { mask32(a, 64, lo, nv); mask32(b, 96, lo, nv); }
-    mt = fmaxf(mt, fmaxf(max32(a), max32(b)));
-    f = raise_max(st, row_ok ? mt * c : -INFINITY, rescale);
-    const float nm = st.m == -INFINITY ? 0.f : -st.m;
-    exp32(a, c, nm, ls, w);
-    exp32(b, c, nm, ls, w + 16);
-    ptx::tmem_st32(p_addr + 32, w);
-    ptx::tmem_ld32(s_addr, a);
-    ptx::tmem_ld32(s_addr + 32, b);
-    ptx::tmem_wait_ld();
-    if (mask) { mask32(a, 0, lo, nv); mask32(b, 32, lo, nv); }
-    exp32(a, c, nm, ls, w);
-    exp32(b, c, nm, ls, w + 16);
-    ptx::tmem_st32(p_addr, w);
-  } else {
-    uint32_t a[kCols / 32][32];
-    float mt = -INFINITY;
+  uint32_t a[N][32];
+  auto load = [&](int c1) {  // scores of columns [c1, c1 + kStep)
 #pragma unroll
-    for (int h = 0; h < kCols / 32; ++h) ptx::tmem_ld32(s_addr + c0 + 32 * h, a[h]);
+    for (int h = 0; h < N; ++h) ptx::tmem_ld32(s_addr + c1 + 32 * h, a[h]);
     ptx::tmem_wait_ld();
+    if (mask)
 #pragma unroll
-    for (int h = 0; h < kCols / 32; ++h) {
-      if (mask) mask32(a[h], c0 + 32 * h, lo, nv);
-      mt = fmaxf(mt, max32(a[h]));
-    }
-    f = raise_max(st, row_ok ? mt * c : -INFINITY, rescale);
-    const float nm = st.m == -INFINITY ? 0.f : -st.m;
-    uint32_t zero[16], w[16];
+      for (int h = 0; h < N; ++h) mask32(a[h], c1 + 32 * h, lo, nv);
+  };
+  float mt = -INFINITY;
+#pragma unroll 1
+  for (int c1 = c0; c1 < c0 + kCols; c1 += kStep) {
+    load(c1);
+#pragma unroll
+    for (int h = 0; h < N; ++h) mt = max32(a[h], mt);
+  }
+  const float f = raise_max(st, row_ok ? mt * c : -INFINITY, rescale);
+  const float nm = st.m == -INFINITY ? 0.f : -st.m;
+  const uint64_t c2 = ptx::pack2(c, c), nm2 = ptx::pack2(nm, nm);
+  uint64_t ls[2] = {0, 0};
+  if constexpr (kCols < kTile) {  // the other copies' keys: weight zero
+    uint32_t zero[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) zero[j] = 0;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {  // word groups of 32 keys
-      const int h = g - c0 / 32;   // warp-uniform
-      if (h < 0 || h >= kCols / 32) {
-        ptx::tmem_st16(p_addr + 16 * g, zero);
-        continue;
-      }
-#pragma unroll
-      for (int hh = 0; hh < kCols / 32; ++hh)
-        if (hh == h) exp32(a[hh], c, nm, ls, w);
-      ptx::tmem_st16(p_addr + 16 * g, w);
-    }
+    for (int g = 0; g < 4; ++g)
+      if (g < c0 / 32 || g >= (c0 + kCols) / 32) ptx::tmem_st16(p_addr + 16 * g, zero);
   }
-  st.l = fmaf(st.l, f, (ls[0] + ls[1]) + (ls[2] + ls[3]));
+  // From the last columns down: P's words of keys 64.. replace S's columns 96..,
+  // which are in registers by then, those of keys 0.. the columns 64..95.  Read
+  // again rather than kept: fewer registers, and a loop of half the code.
+#pragma unroll 1
+  for (int c1 = c0 + kCols - kStep; c1 >= c0; c1 -= kStep) {
+    if (kCols > kStep) load(c1);
+    uint32_t w[16 * N];
+#pragma unroll
+    for (int h = 0; h < N; ++h) exp32(a[h], c2, nm2, ls, w + 16 * h);
+    if constexpr (N == 2)
+      ptx::tmem_st32(p_addr + c1 / 2, w);
+    else
+      ptx::tmem_st16(p_addr + c1 / 2, w);
+  }
+  float l0, l1;
+  ptx::unpack2(ptx::add2(ls[0], ls[1]), l0, l1);
+  st.l = fmaf(st.l, f, l0 + l1);
   return f;
 }
 
@@ -419,6 +422,10 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
     for (int s = 0; s < kSlots; ++s) {
       ptx::mbar_init(bars.full(s), 1);
       ptx::mbar_init(bars.empty(s), 1);
+    }
+    for (int s = 0; s < kSegRing; ++s) {
+      ptx::mbar_init(bars.seg_full(s), 1);
+      ptx::mbar_init(bars.seg_empty(s), kSegReaders);
     }
     ptx::fence_mbar_init();
     start[0] = start[1] = start[2] = 0;
@@ -512,82 +519,135 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  Walk walk{pos, end, base, start[0], start[1], start[2]};
+  Seg* segs = reinterpret_cast<Seg*>(smem + kSegOff);
+  // Segment sg for this warp: false at the end of the schedule (U == 0)
+  auto seg_ready = [&](int sg) {
+    if (!ptx::mbar_wait(bars.seg_full(sg % kSegRing), (sg / kSegRing) & 1)) {
+      record_timeout(p.err, abort_flag);
+      return false;
+    }
+    return segs[sg % kSegRing].U > 0;
+  };
+  auto seg_copy = [&](int sg, Seg& s) {  // and release it
+    if (!__all_sync(full_mask, seg_ready(sg))) return false;
+    s = segs[sg % kSegRing];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bars.seg_empty(sg % kSegRing));
+    return true;
+  };
 
   const uint32_t q_s = sbase;
   auto slot_s = [&](int it) { return sbase + kRingOff + (it % kSlots) * kSlotBytes; };
-  Seg s;
 
   if (warp < 4) {
     ptx::reg_dec<72>();
-    if (warp == 0) {
+    if (warp == 2) {
+      // ================================================== scheduler
+      if (lane == 0) {
+        Walk walk{pos, end, base, start[0], start[1], start[2]};
+        for (int sg = 0;; ++sg) {
+          const int at = sg % kSegRing;
+          Seg s;
+          bool more = walk.next(p, s) && !*abort_flag;
+          if (sg >= kSegRing &&
+              !ptx::mbar_wait(bars.seg_empty(at), ((sg / kSegRing) - 1) & 1)) {
+            if (!*abort_flag) record_timeout(p.err, abort_flag);
+            more = false;
+          }
+          if (!more) s.U = 0;
+          segs[at] = s;
+          bad_page[at] = 0;  // its earlier user is through
+          ptx::mbar_arrive(bars.seg_full(at));
+          if (!more) break;
+        }
+      }
+    } else if (warp == 0) {
       // ================================================== K/V producer
       const int box = min(p.page_size, kTile);  // rows of one box
       const int npg = kTile / box;              // pages a tile touches at most
       const int mh = lane / npg, mi = lane % npg;  // this lane's half and page of a tile
       int it = 0;  // items issued by this CTA so far
       bool stop = false;
-      for (int sg = 0; !stop && walk.next(p, s); ++sg) {
-        if (lane == 0) bad_page[sg % kFlagRing] = 0;
-        __syncwarp();
-        const int32_t* row = p.table + (int64_t)(s.prefix ? 0 : s.b) * p.max_pages;
+      Seg s{}, nx{};
+      // first key of this lane's box of unit tile t, whether it holds keys, its page
+      auto box_key = [&](const Seg& s, int t) { return (s.first + t) * kTile + mi * box; };
+      auto has_keys = [&](const Seg& s, int t) {
+        const int k0 = box_key(s, t);
+        return mh < halves && t < s.Tc && k0 < s.n && k0 + box > s.lo;
+      };
+      auto page_of = [&](const Seg& s, int t) {
+        return t < s.t0 + s.U && has_keys(s, t)
+                   ? p.table[(int64_t)(s.prefix ? 0 : s.b) * p.max_pages +
+                             box_key(s, t) / p.page_size]
+                   : -1;
+      };
+      // one K or V tile of segment sg into the next slot
+      auto issue = [&](int sg, bool is_v, int t, int id) {
+        const uint32_t bar = bars.full(it % kSlots), dst = slot_s(it);
+        if (__any_sync(full_mask, *abort_flag != 0) ||
+            !__all_sync(full_mask,
+                        ptx::mbar_wait(bars.empty(it % kSlots), ((it / kSlots) & 1) ^ 1))) {
+          if (!*abort_flag) record_timeout(p.err, abort_flag);
+          stop = true;
+          return;
+        }
+        if (t == s.Tc) {  // the block rows
+          if (lane == 0) {
+            ptx::mbar_expect_tx(bar, (uint32_t)(halves * p.blk * 128));
+            for (int h = 0; h < halves; ++h)
+              ptx::tma_load_3d(dst + h * kHalfTile, is_v ? &p.tm_vb : &p.tm_kb, bar, 64 * h, s.g,
+                               s.b * p.blk);
+          }
+        } else {
+          const bool has = has_keys(s, t);
+          const bool ok = has && id >= 0 && id < p.pages;
+          if (has && !ok) {
+            bad_page[sg % kFlagRing] = 1;
+            set_err(p.err, ORTHRUS_EINVAL);
+          }
+          const int boxes = __popc(__ballot_sync(full_mask, ok));
+          if (lane == 0) {
+            if (boxes)
+              ptx::mbar_expect_tx(bar, (uint32_t)(boxes * box * 128));
+            else
+              ptx::mbar_arrive(bar);  // nothing to load: every page was refused
+          }
+          __syncwarp();
+          if (ok)
+            ptx::tma_load_2d(dst + mh * kHalfTile + mi * box * 128, is_v ? &p.tm_v : &p.tm_k, bar,
+                             64 * mh,
+                             (id * p.Hkv + s.g) * p.page_size + box_key(s, t) % p.page_size);
+        }
+        ++it;
+      };
+      // the page ids of the next two tiles, and those of the next segment's first
+      // ones, travel while this tile waits for its slot
+      bool more = seg_copy(0, s);
+      int id0 = -1, id1 = -1, id2 = -1;
+      if (more) {
+        id0 = page_of(s, s.t0);
+        id1 = page_of(s, s.t0 + 1);
+        id2 = page_of(s, s.t0 + 2);
+      }
+      for (int sg = 0; more && !stop; ++sg) {
         const int t1 = s.t0 + s.U;
-        // first key of this lane's box of unit tile t, and whether it holds keys
-        auto box_key = [&](int t) { return (s.first + t) * kTile + mi * box; };
-        auto has_keys = [&](int t) {
-          const int k0 = box_key(t);
-          return mh < halves && t < s.Tc && k0 < s.n && k0 + box > s.lo;
-        };
-        auto page_of = [&](int t) {
-          return t < t1 && has_keys(t) ? row[box_key(t) / p.page_size] : -1;
-        };
-        // one K or V tile into the next slot
-        auto issue = [&](bool is_v, int t, int id) {
-          const uint32_t bar = bars.full(it % kSlots), dst = slot_s(it);
-          if (__any_sync(full_mask, *abort_flag != 0) ||
-              !__all_sync(full_mask,
-                          ptx::mbar_wait(bars.empty(it % kSlots), ((it / kSlots) & 1) ^ 1))) {
-            if (!*abort_flag) record_timeout(p.err, abort_flag);
-            stop = true;
-            return;
-          }
-          if (t == s.Tc) {  // the block rows
-            if (lane == 0) {
-              ptx::mbar_expect_tx(bar, (uint32_t)(halves * p.blk * 128));
-              for (int h = 0; h < halves; ++h)
-                ptx::tma_load_3d(dst + h * kHalfTile, is_v ? &p.tm_vb : &p.tm_kb, bar, 64 * h,
-                                 s.g, s.b * p.blk);
-            }
-          } else {
-            const bool has = has_keys(t);
-            const bool ok = has && id >= 0 && id < p.pages;
-            if (has && !ok) {
-              bad_page[sg % kFlagRing] = 1;
-              set_err(p.err, ORTHRUS_EINVAL);
-            }
-            const int boxes = __popc(__ballot_sync(full_mask, ok));
-            if (lane == 0) {
-              if (boxes)
-                ptx::mbar_expect_tx(bar, (uint32_t)(boxes * box * 128));
-              else
-                ptx::mbar_arrive(bar);  // nothing to load: every page was refused
-            }
-            __syncwarp();
-            if (ok)
-              ptx::tma_load_2d(dst + mh * kHalfTile + mi * box * 128, is_v ? &p.tm_v : &p.tm_k,
-                               bar, 64 * mh,
-                               (id * p.Hkv + s.g) * p.page_size + box_key(t) % p.page_size);
-          }
-          ++it;
-        };
-        int id0 = page_of(s.t0), id1 = page_of(s.t0 + 1), id2 = page_of(s.t0 + 2);
-        issue(false, s.t0, id0);
+        issue(sg, false, s.t0, id0);
+        const bool more2 = seg_copy(sg + 1, nx);
+        int n0 = -1, n1 = -1, n2 = -1;
+        if (more2) {
+          n0 = page_of(nx, nx.t0);
+          n1 = page_of(nx, nx.t0 + 1);
+          n2 = page_of(nx, nx.t0 + 2);
+        }
         for (int t = s.t0; t < t1 && !stop; ++t) {
-          const int id3 = page_of(t + 3);
-          if (t + 1 < t1) issue(false, t + 1, id1);
-          if (!stop) issue(true, t, id0);
+          const int id3 = page_of(s, t + 3);
+          if (t + 1 < t1) issue(sg, false, t + 1, id1);
+          if (!stop) issue(sg, true, t, id0);
           id0 = id1; id1 = id2; id2 = id3;
         }
+        more = more2;
+        s = nx;
+        id0 = n0; id1 = n1; id2 = n2;
       }
       // every issued load must have landed before the CTA exits
       for (int x = max(0, it - kSlots); x < it; ++x)
@@ -595,13 +655,15 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
           record_timeout(p.err, abort_flag);
     } else if (warp == 3) {
       // ================================================== Q tiles
-      if (lane == 0) {
-        int sg = 0;
-        for (; walk.next(p, s); ++sg) {
-          if (*abort_flag || (sg > 0 && !ptx::mbar_wait(bars.q_free(), (sg - 1) & 1))) {
-            if (!*abort_flag) record_timeout(p.err, abort_flag);
-            break;
-          }
+      Seg s;
+      int sg = 0;
+      for (; seg_copy(sg, s); ++sg) {
+        if (__any_sync(full_mask, *abort_flag != 0) ||
+            (sg > 0 && !__all_sync(full_mask, ptx::mbar_wait(bars.q_free(), (sg - 1) & 1)))) {
+          if (!*abort_flag) record_timeout(p.err, abort_flag);
+          break;
+        }
+        if (lane == 0) {
           const int rows = s.prefix ? p.ns * p.rowsT : p.rowsT;
           const int reps = s.prefix ? 1 + s.wide : p.copies;
           ptx::mbar_expect_tx(bars.q_full(), (uint32_t)(halves * reps * rows * 128));
@@ -613,9 +675,10 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
                                bars.q_full(), 64 * h, s.g * p.G, b0 * p.blk);
           }
         }
-        if (sg > 0 && !ptx::mbar_wait(bars.q_full(), (sg - 1) & 1))
-          record_timeout(p.err, abort_flag);
+        __syncwarp();
       }
+      if (sg > 0 && !ptx::mbar_wait(bars.q_full(), (sg - 1) & 1))
+        record_timeout(p.err, abort_flag);
     } else if (warp == 1) {
       // ================================================== MMA issuer
       // The whole warp walks and waits, so that descriptors and addresses stay
@@ -672,7 +735,8 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
         ptx::tc_fence_after();
         return true;
       };
-      for (int sg = 0; ok && walk.next(p, s); ++sg) {
+      Seg s;
+      for (int sg = 0; ok && seg_copy(sg, s); ++sg) {
         const int U = s.U;
         ok = all(!*abort_flag && ptx::mbar_wait(bars.q_full(), sg & 1));
         if (!ok) break;
@@ -752,7 +816,14 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
     const int wg_tid = threadIdx.x - 128 - 128 * X;
     bool alive = true;
     int it0 = 0, x0 = 0, ns = 0;  // items and the turn before the segment; S tiles taken
-    for (int sg = 0; walk.next(p, s); ++sg) {
+    for (int sg = 0;; ++sg) {
+      if (!__all_sync(full_mask, seg_ready(sg))) {
+        // the end, or a time-out: meet the others where they would look
+        *agreed = 1;
+        ptx::named_bar_sync(1, 256);
+        break;
+      }
+      const Seg& s = segs[sg % kSegRing];  // released at the segment's end
       const int U = s.U;
       // copies of the rows in the tile, and this thread's row
       const int copies = s.prefix ? 1 : p.copies;
@@ -868,7 +939,7 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
       if (!alive) *agreed = 1;  // so that all leave together
       ptx::named_bar_sync(1, 256);
       const int nf = has_nf[sg % kFlagRing], bad = bad_page[sg % kFlagRing];
-      const int stop = *agreed;
+      if (*agreed) break;
       // m and the factors of the two accumulators for this lane; L over all copies
       float m = st.m, L = st.l, f0 = 1.f, f1 = 0.f;
       bool t0 = true, t1 = false;
@@ -889,7 +960,6 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
       }
       ptx::named_bar_sync(1, 256);
       if (wg_tid == 0 && X == 0) has_nf[(sg + kFlagRing / 2) % kFlagRing] = 0;
-      if (stop) break;
       it0 += 2 * U;
       if (!s.wide) x0 = (x0 + U) & 1;
       ptx::tc_fence_after();
@@ -1002,6 +1072,8 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
         float2* ml = (s.prefix ? p.ml_p : p.ml_t) + (int64_t)slot * srows + prow;
         __stcg(ml, bad ? make_float2(__int_as_float(0x7fffffff), 0.f) : make_float2(m, L));
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars.seg_empty(sg % kSegRing));
     }
   }
   __syncwarp();
