@@ -85,9 +85,11 @@ constexpr int kMergeWays = 4, kMergeDepth = 5;  // (attn_paged_merge)
 constexpr int kHalfTile = kTile * 128;      // one 64-dim half of a K or V tile (16 KB)
 constexpr int kSlotBytes = 2 * kHalfTile;
 constexpr int kQBytes = 2 * kRows * 128;    // one row tile
-constexpr int kXchOff = kQBytes;            // (m, l) exchange and copy sums: the second
-constexpr int kSumOff = kXchOff + 2048;     //   row tile's space, which only wide units
-                                            //   (always before narrow ones) load
+// (m, l) exchange and, over it once it has been read, the copies' sums (two
+// buffers a warpgroup): the second row tile's space, which only wide units
+// (always before narrow ones) load
+constexpr int kXchOff = kQBytes;
+constexpr int kSumBytes = 4 * kRows * 16;
 constexpr int kRingOff = 2 * kQBytes;
 constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
 constexpr int kNumBars = 9 + 2 * kSlots + 2 * kSegRing;
@@ -98,7 +100,7 @@ constexpr int kSegOff = kMiscOff + 256;
 constexpr int kSegBytes = 48;
 constexpr int kSmemBytes = kSegOff + kSegRing * kSegBytes + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
-static_assert(kSumOff + 2 * 4 * kRows * 16 <= kRingOff, "copy sums fit");
+static_assert(kXchOff + 4 * kSumBytes <= kRingOff, "copy sums fit");
 
 struct __align__(64) PagedParams {
   CUtensorMap tm_qp;  // 3D (D, Hq, B*blk), box (64, G, ns*blk)
@@ -362,29 +364,6 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_addr, int c0, int lo, i
   ptx::unpack2(ptx::add2(ls[0], ls[1]), l0, l1);
   st.l = fmaf(st.l, f, l0 + l1);
   return f;
-}
-
-// Sum of the non-finite V elements, zeroed in the tiles, of dim `col` of the
-// block's keys [key, last] in unit tiles [t0, t1).  Rare, and kept out of the way.
-template <int kD>
-__device__ __noinline__ float nonfinite_sum(const PagedParams& p, int b, int g, int n, int key,
-                                            int last, int first, int Tc, int t0, int t1,
-                                            int col) {
-  float sum = 0.f;
-  for (; key <= last; ++key) {
-    const __nv_bfloat16* vr;
-    const int tile = p.v_blk ? Tc : key / kTile - first;
-    if (tile < t0 || tile >= t1) continue;
-    if (p.v_blk) {
-      vr = p.v_blk + ((int64_t)(b * p.blk + key - n) * p.Hkv + g) * kD;
-    } else {
-      const int id = p.table[(int64_t)b * p.max_pages + key / p.page_size];
-      vr = p.v_pages + (((int64_t)id * p.Hkv + g) * p.page_size + key % p.page_size) * kD;
-    }
-    const float x = __bfloat162float(vr[col]);
-    if (!isfinite(x)) sum += x;
-  }
-  return sum;
 }
 
 template <int kD>
@@ -814,11 +793,17 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t s_addr = lane_addr + X * kTile;
     const int wg_tid = threadIdx.x - 128 - 128 * X;
+    // this thread's row: in a tail's tile (copy of `span` lanes, its row rc), and in a
+    // prefix tile (sequence pj of the tile, row pt of it)
+    const int span_t = kRows / p.copies, rc_t = r % span_t, c0_t = r - rc_t;
+    const int i_t = rc_t < p.rowsT ? rc_t / p.G : 0;
+    const int pj = r / p.rowsT, pt = r - pj * p.rowsT, i_p = pt / p.G;
     bool alive = true;
     int it0 = 0, x0 = 0, ns = 0;  // items and the turn before the segment; S tiles taken
     for (int sg = 0;; ++sg) {
       if (!__all_sync(full_mask, seg_ready(sg))) {
         // the end, or a time-out: meet the others where they would look
+        ptx::named_bar_sync(1, 256);
         *agreed = 1;
         ptx::named_bar_sync(1, 256);
         break;
@@ -827,19 +812,19 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
       const int U = s.U;
       // copies of the rows in the tile, and this thread's row
       const int copies = s.prefix ? 1 : p.copies;
-      const int span = kRows / copies;  // lanes and columns of one copy
-      const int c0 = (r / span) * span;  // first column of its keys
-      const int rc = r % span;
-      int rows = p.rowsT, bq = s.b, rt = rc;
+      const int span = s.prefix ? kRows : span_t;  // lanes and columns of one copy
+      const int c0 = s.prefix ? 0 : c0_t;          // first column of its keys
+      const int rc = r - c0;
+      int rows = p.rowsT, bq = s.b, rt = rc_t, i_blk = i_t;
       if (s.prefix) {  // row tile s.b + X (wide) or s.b
         const int b0 = (s.b + (s.wide ? X : 0)) * p.ns;
         rows = min(p.ns, p.B - b0) * p.rowsT;
-        bq = b0 + (rc < rows ? rc / p.rowsT : 0);
-        rt = rc % p.rowsT;
+        bq = b0 + (r < rows ? pj : 0);
+        rt = pt;
+        i_blk = i_p;
       }
       const bool row_ok = rc < rows;
-      if (!row_ok) rt = 0;
-      const int i_blk = rt / p.G;
+      if (!row_ok) rt = i_blk = 0;
       // cache keys this row sees: [lo, lim)
       int lim = s.n;
       if (s.prefix) {
@@ -852,7 +837,7 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
       const int fence = s.prefix || !p.causal ? 0x7fffffff : (p.v_blk ? s.n : s.n - p.blk) + 1;
       // any row of this warp in use (rows past the tile's are padding: their
       // scores are left unmasked and their results unread)
-      const bool warp_rows = (quad * 32) % span < rows;
+      const bool warp_rows = ((quad * 32) & (span - 1)) < rows;
       RowState st{-INFINITY, 0.f};
       int done = 0;  // tiles of this segment this warpgroup has taken
       for (int u = s.wide ? 0 : (x0 ^ X); alive && u < U; u += s.wide ? 1 : 2, ++done) {
@@ -935,6 +920,7 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
       }
       // every thread gets here even after a time-out
       float2* xch = reinterpret_cast<float2*>(smem + kXchOff);
+      ptx::named_bar_sync(1, 256);  // the previous segment's sums have been read
       if (!s.wide) xch[X * kRows + r] = done ? make_float2(st.m, st.l) : make_float2(-INFINITY, 0.f);
       if (!alive) *agreed = 1;  // so that all leave together
       ptx::named_bar_sync(1, 256);
@@ -944,14 +930,24 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
       float m = st.m, L = st.l, f0 = 1.f, f1 = 0.f;
       bool t0 = true, t1 = false;
       if (!s.wide) {
-        m = -INFINITY;
-        for (int i = 0; i < 2 * copies; ++i)
-          m = fmaxf(m, xch[(i & 1) * kRows + (i >> 1) * span + rc].x);
-        L = 0.f;
-        // a sum may be NaN with a maximum of -inf (every visible score NaN)
-        auto part = [&](float2 a) { return a.x == -INFINITY ? a.y : a.y * ptx::ex2(a.x - m); };
-        for (int i = 0; i < 2 * copies; ++i)
-          L += part(xch[(i & 1) * kRows + (i >> 1) * span + rc]);
+        auto gather = [&](auto nc) {  // over the copies and both warpgroups
+          constexpr int kC = decltype(nc)::value;
+          float2 a[2 * kC];
+#pragma unroll
+          for (int i = 0; i < 2 * kC; ++i)
+            a[i] = xch[(i & 1) * kRows + (i >> 1) * (kRows / kC) + rc];
+          m = a[0].x;
+#pragma unroll
+          for (int i = 1; i < 2 * kC; ++i) m = fmaxf(m, a[i].x);
+          L = 0.f;
+          // a sum may be NaN with a maximum of -inf (every visible score NaN)
+#pragma unroll
+          for (int i = 0; i < 2 * kC; ++i)
+            L += a[i].x == -INFINITY ? a[i].y : a[i].y * ptx::ex2(a[i].x - m);
+        };
+        if (copies == 4) gather(std::integral_constant<int, 4>{});
+        else if (copies == 2) gather(std::integral_constant<int, 2>{});
+        else gather(std::integral_constant<int, 1>{});
         const float2 a0 = xch[r], a1 = xch[kRows + r];
         f0 = a0.x == -INFINITY ? 0.f : ptx::ex2(a0.x - m);
         f1 = a1.x == -INFINITY ? 0.f : ptx::ex2(a1.x - m);
@@ -982,11 +978,25 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
         constexpr int kN = decltype(n)::value;
         if (!row_ok || bad) return;
         if (nf) {
+          // non-finite V elements, zeroed in the tiles, of the block's keys that
+          // this row sees
+          const int last = p.v_blk ? s.n + i_blk : lim - 1;
+          for (int key = p.v_blk ? s.n + 1 : max(s.n - p.blk + 1, 0); key <= last; ++key) {
+            const __nv_bfloat16* vr;
+            const int tile = p.v_blk ? s.Tc : key / kTile - s.first;
+            if (tile < s.t0 || tile >= s.t0 + s.U) continue;
+            if (p.v_blk) {
+              vr = p.v_blk + ((int64_t)(s.b * p.blk + key - s.n) * p.Hkv + s.g) * kD;
+            } else {
+              const int id = p.table[(int64_t)s.b * p.max_pages + key / p.page_size];
+              vr = p.v_pages + (((int64_t)id * p.Hkv + s.g) * p.page_size + key % p.page_size) * kD;
+            }
 #pragma unroll
-          for (int j = 0; j < kN; ++j)
-            v[j] += nonfinite_sum<kD>(p, s.b, s.g, s.n, p.v_blk ? s.n + 1 : max(s.n - p.blk + 1, 0),
-                                      p.v_blk ? s.n + i_blk : lim - 1, s.first, s.Tc, s.t0,
-                                      s.t0 + s.U, col + j);
+            for (int j = 0; j < kN; ++j) {
+              const float x = __bfloat162float(vr[col + j]);
+              if (!isfinite(x)) v[j] += x;
+            }
+          }
         }
         if (direct) {
 #pragma unroll
@@ -1008,35 +1018,40 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
       auto take = [&](int col, float (&v)[16]) {
         if (!warp_rows) return;
         // selects, not products: an O that no tile wrote may hold anything
-        uint32_t o[16];
-        ptx::tmem_ld16_sync(oa + col, o);
+        uint32_t o0[16], o1[16];
+        ptx::tmem_ld16(oa + col, o0);
+        ptx::tmem_ld16(oa + (s.wide ? 0 : kD) + col, o1);
+        ptx::tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = t0 ? f0 * __uint_as_float(o[j]) : 0.f;
-        if (s.wide) return;
-        ptx::tmem_ld16_sync(oa + kD + col, o);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = t1 ? fmaf(f1, __uint_as_float(o[j]), v[j]) : v[j];
+        for (int j = 0; j < 16; ++j) {
+          v[j] = t0 ? f0 * __uint_as_float(o0[j]) : 0.f;
+          v[j] = t1 ? fmaf(f1, __uint_as_float(o1[j]), v[j]) : v[j];
+        }
       };
       // wide: all columns; otherwise the warpgroup's half of them
       const int col0 = s.wide ? 0 : X * (kD / 2), cols = s.wide ? kD : kD / 2;
+      auto read_out = [&](int cb) {  // O is read: the next segment may overwrite it
+        if (cb + 16 < cols) return;
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bars.o_free());
+      };
       // sum over kC copies, 16 columns at a time: the lanes exchange 16-byte
-      // chunks, then lane r holds 16 / kC columns of row rc
+      // chunks, then lane r holds 16 / kC columns of row rc.  Two buffers by
+      // turns, so that one barrier a turn is enough.
       auto drain_copies = [&](auto nc) {
         constexpr int kC = decltype(nc)::value, kN = 16 / kC;
-        float4* sum = reinterpret_cast<float4*>(smem + kSumOff) + X * 4 * kRows;
+        const int q0 = c0 / (kRows / kC);
 #pragma unroll 1
         for (int cb = 0; cb < kD / 2; cb += 16) {
+          float4* sum = reinterpret_cast<float4*>(smem + kXchOff) +
+                        (X * 2 + (cb >> 4 & 1)) * 4 * kRows;
           float v[16];
           take(col0 + cb, v);
-          if (cb + 16 == kD / 2) {
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(bars.o_free());
-          }
+          read_out(cb);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             sum[j * kRows + r] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           ptx::named_bar_sync(2 + X, 128);
-          const int q0 = r / span;
 #pragma unroll
           for (int j = 0; j < kN / 4; ++j) {
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1048,7 +1063,6 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
             v[4 * j] = a.x; v[4 * j + 1] = a.y; v[4 * j + 2] = a.z; v[4 * j + 3] = a.w;
           }
           put(std::integral_constant<int, kN>{}, col0 + cb + q0 * kN, v);
-          ptx::named_bar_sync(2 + X, 128);
         }
       };
       if (copies == 4) {
@@ -1060,10 +1074,7 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
         for (int cb = 0; cb < cols; cb += 16) {
           float v[16];
           take(col0 + cb, v);
-          if (cb + 16 == cols) {  // O is read: the next segment may overwrite it
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(bars.o_free());
-          }
+          read_out(cb);
           put(std::integral_constant<int, 16>{}, col0 + cb, v);
         }
       }
