@@ -37,9 +37,11 @@
 //                belongs to warpgroup X, otherwise they take turns on the tiles
 // S(u) = Q K(u)^T goes to the warpgroup's own 128 TMEM columns; P(u) replaces
 // the upper half of S(u) as bf16 and is the A operand of O_X += P(u) V(u)
-// straight from tensor memory, which leaves shared memory to the ring.  The
-// next S of a warpgroup is issued behind its P V, so one commit says that both
-// are done and no further barriers guard the buffers.  Producers run ahead over
+// straight from tensor memory, which leaves shared memory to the ring; its two
+// halves are announced apart, so that half of P V runs under the exponentials.
+// The next S of a warpgroup is issued behind its P V (the tensor core works a
+// CTA's products off in the order of issue), so one commit says that both are
+// done and no further barriers guard the buffers.  Producers run ahead over
 // unit boundaries.  The first warpgroup hands registers to the two softmax
 // ones (72 + 2 x 216 = 3 x 168 a thread).
 // TMEM (512 columns): S_0/P_0 [0,128) S_1/P_1 [128,256) O_0 [256,256+D) O_1
@@ -92,7 +94,7 @@ constexpr int kXchOff = kQBytes;
 constexpr int kSumBytes = 4 * kRows * 16;
 constexpr int kRingOff = 2 * kQBytes;
 constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
-constexpr int kNumBars = 9 + 2 * kSlots + 2 * kSegRing;
+constexpr int kNumBars = 11 + 2 * kSlots + 2 * kSegRing;
 constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
 // TMEM address, abort flag, start of the walk, scan words, segment flags; the
 // ring of segments
@@ -136,11 +138,12 @@ struct Bars {
   __device__ uint32_t seg_done() const { return at(3); }  // every P V of the segment is done
   __device__ uint32_t exit_done() const { return at(4); }
   __device__ uint32_t s_full(int x) const { return at(5 + x); }  // S_X there, P_X V done
-  __device__ uint32_t p_full(int x) const { return at(7 + x); }  // P_X there
-  __device__ uint32_t full(int s) const { return at(9 + s); }
-  __device__ uint32_t empty(int s) const { return at(9 + kSlots + s); }
-  __device__ uint32_t seg_full(int s) const { return at(9 + 2 * kSlots + s); }
-  __device__ uint32_t seg_empty(int s) const { return at(9 + 2 * kSlots + kSegRing + s); }
+  __device__ uint32_t p_high(int x) const { return at(7 + x); }  // P_X of keys 64.. there
+  __device__ uint32_t p_low(int x) const { return at(9 + x); }   // and of keys 0..63
+  __device__ uint32_t full(int s) const { return at(11 + s); }
+  __device__ uint32_t empty(int s) const { return at(11 + kSlots + s); }
+  __device__ uint32_t seg_full(int s) const { return at(11 + 2 * kSlots + s); }
+  __device__ uint32_t seg_empty(int s) const { return at(11 + 2 * kSlots + kSegRing + s); }
 };
 
 __device__ __forceinline__ void record_timeout(int32_t* err, volatile int* abort_flag) {
@@ -274,18 +277,21 @@ __device__ __forceinline__ float max32(const uint32_t (&sv)[32], float m) {
   }
   return fmaxf(a, b);
 }
-// weights 2^(s c + nm) of 32 scores as bf16 pairs; adds them, two a time, to ls
+// weights 2^(s c + nm) of 32 scores as bf16 pairs; adds them, two at a time, to ls
+// (a quarter or half of the exponentials as a cubic on the FMA pipe instead of the
+// special-function unit was slower: 129 -> 134 and 148 us at 128 requests behind
+// a 16k prefix -- instructions, not that unit, bound the softmax)
 __device__ __forceinline__ void exp32(const uint32_t (&sv)[32], uint64_t c, uint64_t nm,
                                       uint64_t (&ls)[2], uint32_t* w) {
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) {
+  for (int j = 0; j < 16; ++j) {
     float x, y;
-    ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), c, nm),
-                 x, y);
+    ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])),
+                           c, nm), x, y);
     x = ptx::ex2(x);
     y = ptx::ex2(y);
-    ls[(j >> 1) & 1] = ptx::add2(ls[(j >> 1) & 1], ptx::pack2(x, y));
-    w[j >> 1] = ptx::pack_bf16x2(x, y);
+    ls[j & 1] = ptx::add2(ls[j & 1], ptx::pack2(x, y));
+    w[j] = ptx::pack_bf16x2(x, y);
   }
 }
 
@@ -309,11 +315,14 @@ __device__ __forceinline__ float raise_max(RowState& st, float ms, bool& any) {
 }
 
 // Softmax of one tile for the row of this thread: kCols keys from column c0 of
-// the tile, of which the row sees [lo, nv).  Reads S, writes P (zero in the
-// other columns) and returns the factor for O.
-template <int kCols>
-__device__ __forceinline__ float softmax_tile(uint32_t s_addr, int c0, int lo, int nv, float c,
-                                              bool row_ok, RowState& st, bool& rescale) {
+// the tile, of which the row sees [lo, nv).  Reads S, rescales O (if it holds
+// anything) and writes P, zero in the other columns.  With a barrier `early` (whole
+// tiles of one copy only) P of keys 64.. is announced on it as soon as it is there,
+// so that its product with V runs under the exponentials of the rest.
+template <int kCols, int kD>
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, int c0, int lo, int nv, float c,
+                                             bool row_ok, RowState& st, uint32_t o_addr,
+                                             bool has_o, uint32_t early) {
   constexpr int kStep = kCols < 64 ? kCols : 64;  // columns in registers at a time
   constexpr int N = kStep / 32;
   const uint32_t p_addr = s_addr + 64;
@@ -334,7 +343,18 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_addr, int c0, int lo, i
 #pragma unroll
     for (int h = 0; h < N; ++h) mt = max32(a[h], mt);
   }
+  bool rescale;
   const float f = raise_max(st, row_ok ? mt * c : -INFINITY, rescale);
+  if (rescale && has_o) {
+#pragma unroll 1
+    for (int cb = 0; cb < kD; cb += 32) {
+      ptx::tmem_ld32_sync(o_addr + cb, a[0]);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) a[0][j] = __float_as_uint(__uint_as_float(a[0][j]) * f);
+      ptx::tmem_st32(o_addr + cb, a[0]);
+    }
+    if (kCols == kStep) load(c0);
+  }
   const float nm = st.m == -INFINITY ? 0.f : -st.m;
   const uint64_t c2 = ptx::pack2(c, c), nm2 = ptx::pack2(nm, nm);
   uint64_t ls[2] = {0, 0};
@@ -359,11 +379,15 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_addr, int c0, int lo, i
       ptx::tmem_st32(p_addr + c1 / 2, w);
     else
       ptx::tmem_st16(p_addr + c1 / 2, w);
+    if (kCols == 128 && c1 > 0 && early) {
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(early);
+    }
   }
   float l0, l1;
   ptx::unpack2(ptx::add2(ls[0], ls[1]), l0, l1);
   st.l = fmaf(st.l, f, l0 + l1);
-  return f;
 }
 
 template <int kD>
@@ -396,7 +420,8 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
     ptx::mbar_init(bars.exit_done(), 1);
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(bars.s_full(s), 1);
-      ptx::mbar_init(bars.p_full(s), 128);
+      ptx::mbar_init(bars.p_high(s), 128);
+      ptx::mbar_init(bars.p_low(s), 128);
     }
     for (int s = 0; s < kSlots; ++s) {
       ptx::mbar_init(bars.full(s), 1);
@@ -689,14 +714,15 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
         }
         __syncwarp();
       };
-      // O_x (+)= P_x V, P_x from tensor memory, 16 keys = 8 columns a step
-      auto pv_tile = [&](int x, int it, bool fresh) {
+      // O_x (+)= P_x V over keys 64 half .., P_x from tensor memory, 16 keys = 8
+      // columns a step.  The high half comes first
+      auto pv_half = [&](int x, int it, int half, bool fresh) {
         const uint64_t b = vd + (uint64_t)((it % kSlots) * (kSlotBytes >> 4));
         if (lead) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            ptx::mma_ts(tmem + kOCol + x * kD, tmem + x * kTile + 64 + 8 * k, b + k * (2048 >> 4),
-                        id_pv, (!fresh || k > 0) ? 1u : 0u);
+          for (int k = 0; k < 4; ++k)
+            ptx::mma_ts(tmem + kOCol + x * kD, tmem + x * kTile + 64 + 32 * half + 8 * k,
+                        b + (4 * half + k) * (2048 >> 4), id_pv, (!fresh || k > 0) ? 1u : 0u);
         }
         __syncwarp();
       };
@@ -708,10 +734,18 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
       int it0 = 0, x0 = 0;   // items and the turn before this segment
       int np0 = 0, np1 = 0;  // P tiles taken of each warpgroup
       bool ok = true;
-      auto p_ready = [&](int x) {
-        if (!ptx::mbar_wait(bars.p_full(x), (x ? np1 : np0) & 1)) return false;
-        if (x) ++np1; else ++np0;
+      auto p_ready = [&](uint32_t bar, int x) {
+        if (!ptx::mbar_wait(bar, (x ? np1 : np0) & 1)) return false;
         ptx::tc_fence_after();
+        return true;
+      };
+      // the whole of O_x += P_x V as its halves arrive
+      auto pv_tile = [&](int x, int it, bool fresh) {
+        if (!all(!*abort_flag && p_ready(bars.p_high(x), x) && landed(it))) return false;
+        pv_half(x, it, 1, fresh);
+        if (!all(p_ready(bars.p_low(x), x))) return false;
+        pv_half(x, it, 0, false);
+        if (x) ++np1; else ++np0;
         return true;
       };
       Seg s;
@@ -730,17 +764,15 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
           for (int u = 0; ok && u < U; ++u) {
             const int vi = v_item(it0, u, U), ki = k_item(it0, u + 1);
             const bool more = u + 1 < U;
-            ok = all(!*abort_flag && p_ready(0) && landed(vi));
+            ok = pv_tile(0, vi, u == 0);
             if (!ok) break;
-            pv_tile(0, vi, u == 0);
             if (more) {
               ok = all(landed(ki));
               if (!ok) break;
               s_tile(0, 0, ki);
             }
-            ok = all(p_ready(1));
+            ok = pv_tile(1, vi, u == 0);
             if (!ok) break;
-            pv_tile(1, vi, u == 0);
             commit(bars.empty(vi % kSlots));
             if (more) {
               s_tile(1, 1, ki);
@@ -761,9 +793,8 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
           if (ok && sg > 0) ok = all(ptx::mbar_wait(bars.o_free(), (sg - 1) & 1));
           for (int u = 0; ok && u < U; ++u) {
             const int x = (x0 + u) & 1, vi = v_item(it0, u, U);
-            ok = all(!*abort_flag && p_ready(x) && landed(vi));
+            ok = pv_tile(x, vi, u < 2);
             if (!ok) break;
-            pv_tile(x, vi, u < 2);
             commit(bars.empty(vi % kSlots));
             if (u + 2 < U) {
               const int ki = k_item(it0, u + 2);
@@ -854,30 +885,25 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
         const int lo_tile = blk_tile ? 0 : max(0, s.lo - k0);
         int nv = blk_tile ? (p.causal ? i_blk + 1 : p.blk) : lim - k0;
         nv = row_ok ? max(0, min(nv, nv_tile)) : kTile;
-        if (warp_rows) {
-          bool rescale;
-          float f;
-          const float sc = p.scale_log2;
-          if (copies == 1)
-            f = softmax_tile<128>(s_addr, 0, lo_tile, nv, sc, row_ok, st, rescale);
-          else if (copies == 2)
-            f = softmax_tile<64>(s_addr, c0, lo_tile, nv, sc, row_ok, st, rescale);
-          else
-            f = softmax_tile<32>(s_addr, c0, lo_tile, nv, sc, row_ok, st, rescale);
-          if (rescale && done > 0) {  // O holds this warpgroup's earlier tiles
-#pragma unroll 1
-            for (int cb = 0; cb < kD / 32; ++cb) {
-              uint32_t o[32];
-              ptx::tmem_ld32_sync(lane_addr + kOCol + X * kD + cb * 32, o);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              ptx::tmem_st32(lane_addr + kOCol + X * kD + cb * 32, o);
-            }
-          }
-          ptx::tmem_wait_st();
-        }
         const int fz = blk_tile ? (p.causal ? 1 : kTile) : max(lo_tile, fence - k0);
-        if ((nv_tile < kTile || lo_tile > 0 || fz < nv_tile) && !(s.wide && X)) {
+        const bool mend_v = nv_tile < kTile || lo_tile > 0 || fz < nv_tile;
+        const bool early = copies == 1 && !mend_v;
+        if (warp_rows) {
+          const float sc = p.scale_log2;
+          const uint32_t o_addr = lane_addr + kOCol + X * kD;
+          const bool has_o = done > 0;  // O holds this warpgroup's earlier tiles
+          if (copies == 1)
+            softmax_tile<128, kD>(s_addr, 0, lo_tile, nv, sc, row_ok, st, o_addr, has_o,
+                                  early ? bars.p_high(X) : 0u);
+          else if (copies == 2)
+            softmax_tile<64, kD>(s_addr, c0, lo_tile, nv, sc, row_ok, st, o_addr, has_o, 0u);
+          else
+            softmax_tile<32, kD>(s_addr, c0, lo_tile, nv, sc, row_ok, st, o_addr, has_o, 0u);
+          ptx::tmem_wait_st();
+        } else if (early) {
+          ptx::mbar_arrive(bars.p_high(X));
+        }
+        if (mend_v && !(s.wide && X)) {
           // (a wide tile's V serves both warpgroups: the first prepares it, and
           // its product is issued first)
           const int vi = v_item(it0, u, U);
@@ -911,7 +937,8 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
           ptx::fence_proxy_async_smem();
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(bars.p_full(X));
+        if (!early) ptx::mbar_arrive(bars.p_high(X));
+        ptx::mbar_arrive(bars.p_low(X));
       }
       // ---- the segment's O, row maxima and sums
       if (alive && !__all_sync(full_mask, ptx::mbar_wait(bars.seg_done(), sg & 1))) {
