@@ -683,58 +683,56 @@ def _packer(cls):
 _pack_filter, _pack_rope = _packer(FilterArgs), _packer(RopeArgs)
 _pack_append, _pack_paged_attn = _packer(AppendArgs), _packer(PagedAttnArgs)
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
 _i32, _f32, _f64 = torch.int32, torch.float32, torch.float64
 
 
-def _refuse(name, t, dtype, device, shape):
+def _refuse(name, t, dtype, index, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device (no CPU path)")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _need(name, t, dtype, device, shape=None):
+def _need(name, t, dtype, index, shape=None):
     """Pointer of a contiguous tensor of that type, device and shape (None: any)."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device
+    if (t.dtype is not dtype or t.get_device() != index
             or (shape is not None and t.shape != shape) or not t.is_contiguous()):
-        _refuse(name, t, dtype, device, shape)
+        _refuse(name, t, dtype, index, shape)
     return t.data_ptr()
 
 
-def _opt(name, t, dtype, device, shape=None):
+def _opt(name, t, dtype, index, shape=None):
     """The same for an optional tensor: 0 if it is not given."""
-    return 0 if t is None else _need(name, t, dtype, device, shape)
+    return 0 if t is None else _need(name, t, dtype, index, shape)
 
 
-def _lead(name, t):
-    """(device, dtype code) of a call's main tensor."""
-    dev = t.device
-    if dev.type != "cuda":
+def _lead(t):
+    """(device index, dtype code) of a call's main tensor."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device (no CPU path)")
     code = _DT.get(t.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return dev, code
+    return index, code
 
 
-def _elsewhere(device, stream):
-    """Context for a call that does not run on the current device and stream, else
-    None: it allocates and launches where its tensors and stream are."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("the stream belongs to another device than the tensors")
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device)
-    return None
+def _elsewhere(index, stream):
+    """Context for a call that does not run on the current device and stream: it
+    allocates and launches where its tensors and stream are."""
+    if stream is None:
+        return torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)
 
 
 class _StreamWorkspace(Workspace):
@@ -755,13 +753,13 @@ class _StreamWorkspace(Workspace):
         return self.buf
 
 
-def _stream_ws(ws, device, op):
+def _stream_ws(ws, index, op):
     """Caller's workspace, else the current stream's default for this op."""
     if ws is None:
-        key = (device.index, op, _raw_stream(device.index))
+        key = (index, op, _raw_stream(index))
         ws = _default_ws.get(key)
         if ws is None:
-            ws = _default_ws[key] = _StreamWorkspace(device)
+            ws = _default_ws[key] = _StreamWorkspace(torch.device("cuda", index))
     return ws
 
 
@@ -793,19 +791,18 @@ def rope(x, positions, inv_freq, *, layout=ROPE_HALF, mscale=1.0, inverse=False,
     may be views with any row and head strides (unit stride inside a head);
     ``out=x`` rotates in place.  ``inverse`` turns back: the gradient with
     respect to x of the call with the same arguments."""
-    dev, dt = _lead("x", x)
+    dev, dt = _lead(x)
     if x.dim() != 3:
         raise ValueError("x must be [rows, H, D]")
-    where = _elsewhere(dev, stream)
-    if where is not None:
-        with where:
+    if stream is not None or dev != _device():
+        with _elsewhere(dev, stream):
             return rope(x, positions, inv_freq, layout=layout, mscale=mscale, inverse=inverse,
                         out=out)
     rows, H, D = x.shape
     xr, xh, xd = x.stride()
     if out is None:
-        out = torch.empty(rows, H, D, dtype=x.dtype, device=dev)
-    elif out.dtype is not x.dtype or out.device != dev or out.shape != x.shape:
+        out = torch.empty(rows, H, D, dtype=x.dtype, device=x.device)
+    elif out.dtype is not x.dtype or out.get_device() != dev or out.shape != x.shape:
         _refuse("out", out, x.dtype, dev, x.shape)
     yr, yh, yd = out.stride()
     if (xd != 1 or yd != 1) and D > 1 and rows and H:
@@ -815,7 +812,7 @@ def rope(x, positions, inv_freq, *, layout=ROPE_HALF, mscale=1.0, inverse=False,
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     a = _pack_rope(dt, layout, rows, H, D, rot, bool(inverse), mscale, x.data_ptr(), xr, xh,
                    out.data_ptr(), yr, yh, pos, freq)
-    rc = lib().orthrus_rope(a, _raw_stream(dev.index))
+    rc = lib().orthrus_rope(a, _raw_stream(dev))
     if rc:
         raise OrthrusError("orthrus_rope", rc)
     return out
@@ -834,10 +831,9 @@ def paged_append(k, v, k_pages, v_pages, page_table, ctx_lens, *, n_rows=None, r
     (q [rows, Hq, D]) and row_starts int32 [B + 1].  Rows may be strided views
     of one projection's output.  ``advance`` adds the rows taken to ctx_lens.
     Returns q_out (None without q)."""
-    dev, dt = _lead("k", k)
-    where = _elsewhere(dev, stream)
-    if where is not None:
-        with where:
+    dev, dt = _lead(k)
+    if stream is not None or dev != _device():
+        with _elsewhere(dev, stream):
             return paged_append(k, v, k_pages, v_pages, page_table, ctx_lens, n_rows=n_rows,
                                 row_starts=row_starts, inv_freq=inv_freq, layout=layout,
                                 mscale=mscale, q=q, q_out=q_out, advance=advance, err=err,
@@ -852,7 +848,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, ctx_lens, *, n_rows=None, r
     if dims != (3 if ragged else 4) + layered or v.shape != k.shape:
         raise ValueError("k and v must be [B, blk, Hkv, D], or [rows, Hkv, D] with row_starts, "
                          "with an optional leading layer dimension")
-    if v.dtype is not ty or v.device != dev:
+    if v.dtype is not ty or v.get_device() != dev:
         _refuse("v", v, ty, dev, None)
     pools = k_pages.shape
     if len(pools) != 4 + layered or v_pages.shape != pools:
@@ -893,34 +889,37 @@ def paged_append(k, v, k_pages, v_pages, page_table, ctx_lens, *, n_rows=None, r
                 raise ValueError(f"{name}: the rows of consecutive blocks must be evenly spaced")
         return (st[0] if layered else 0), row, st[-2]
 
-    ks, vs = strides(k, "k"), strides(v, "v")
-    Hq, qp, qo, qs = 0, 0, 0, (0, 0, 0)
-    if q is not None:
+    ks = strides(k, "k")
+    vs = strides(v, "v")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        Hq = qp = qo = qr = qh = 0
+    else:
         qshape = q.shape
         if layered or qshape[:-2] != shape[:-2] or qshape[-1] != D:
             raise ValueError("q must be shaped like k but for its heads, without layers")
-        if q.dtype is not ty or q.device != dev:
+        if q.dtype is not ty or q.get_device() != dev:
             _refuse("q", q, ty, dev, None)
-        Hq, qp, qs = qshape[-2], q.data_ptr(), strides(q, "q")
+        Hq, qp = qshape[-2], q.data_ptr()
+        _, qr, qh = strides(q, "q")
         if q_out is None:
-            q_out = torch.empty(qshape, dtype=ty, device=dev)
+            q_out = torch.empty(qshape, dtype=ty, device=k.device)
         qo = _need("q_out", q_out, ty, dev, qshape)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
     ws = nbytes = 0
     if advance:
         buf = _stream_ws(workspace, dev, "paged_append").get(256)
         ws, nbytes = buf.data_ptr(), buf.numel()
     a = _pack_append(dt, layers, B, blk, rows, Hq, Hkv, D, page_size, pages, max_pages,
                      0 if inv_freq is None else 2 * inv_freq.numel(), layout, bool(advance),
-                     mscale, k.data_ptr(), v.data_ptr(), qp, *ks, *vs, qs[1], qs[2], qo, kp, vp,
+                     mscale, k.data_ptr(), v.data_ptr(), qp, *ks, *vs, qr, qh, qo, kp, vp,
                      pages_stride, _need("page_table", page_table, _i32, dev),
                      _need("ctx_lens", ctx_lens, _i32, dev, (B,)),
                      _opt("n_rows", n_rows, _i32, dev, (B,)),
                      _opt("row_starts", row_starts, _i32, dev, (B + 1,)),
                      _opt("inv_freq", inv_freq, _f64, dev), _opt("err", err, _i32, dev), ws,
                      nbytes)
-    rc = lib().orthrus_paged_append(a, _raw_stream(dev.index))
+    rc = lib().orthrus_paged_append(a, _raw_stream(dev))
     if rc:
         raise OrthrusError("orthrus_paged_append", rc)
     return q_out
@@ -937,10 +936,9 @@ def paged_block_attn(q, k_blk, v_blk, k_pages, v_pages, page_table, ctx_lens, ma
     ``shared_prefix``: keys common to the whole batch, read once through row 0
     of the table.  max_ctx bounds every ctx_lens entry (default: the table's
     reach).  Returns out [B, blk, Hq, D]."""
-    dev, dt = _lead("q", q)
-    where = _elsewhere(dev, stream)
-    if where is not None:
-        with where:
+    dev, dt = _lead(q)
+    if stream is not None or dev != _device():
+        with _elsewhere(dev, stream):
             return paged_block_attn(q, k_blk, v_blk, k_pages, v_pages, page_table, ctx_lens,
                                     mask_mode, shared_prefix=shared_prefix, out=out, scale=scale,
                                     max_ctx=max_ctx, err=err, workspace=workspace)
@@ -957,7 +955,7 @@ def paged_block_attn(q, k_blk, v_blk, k_pages, v_pages, page_table, ctx_lens, ma
     max_pages = page_table.shape[1]
     block = (B, blk, Hkv, D)
     if out is None:
-        out = torch.empty(shape, dtype=ty, device=dev)
+        out = torch.empty(shape, dtype=ty, device=q.device)
     if max_ctx is None:
         max_ctx = max_pages * page_size
     if scale is None:
@@ -975,7 +973,7 @@ def paged_block_attn(q, k_blk, v_blk, k_pages, v_pages, page_table, ctx_lens, ma
     if need:
         buf = _stream_ws(workspace, dev, "paged_attn").get(need)
         ws, nbytes = buf.data_ptr(), buf.numel()
-    rc = L.orthrus_paged_attn(_pack_paged_attn(*args, ws, nbytes), _raw_stream(dev.index))
+    rc = L.orthrus_paged_attn(_pack_paged_attn(*args, ws, nbytes), _raw_stream(dev))
     if rc:
         raise OrthrusError("orthrus_paged_attn", rc)
     return out
@@ -988,12 +986,11 @@ def vocab_sample_filtered(logits, u, *, temperature=None, top_k=None, top_p=None
     orthrus.h).  Each parameter is a number for all rows or a device tensor
     [rows] (top_k int32, the others float32); None leaves it out.  ``logprob``
     float32 [rows] receives the token's log-probability among those kept."""
-    dev, dt = _lead("logits", logits)
+    dev, dt = _lead(logits)
     if logits.dim() != 2:
         raise ValueError("logits must be [rows, vocab]")
-    where = _elsewhere(dev, stream)
-    if where is not None:
-        with where:
+    if stream is not None or dev != _device():
+        with _elsewhere(dev, stream):
             return vocab_sample_filtered(logits, u, temperature=temperature, top_k=top_k,
                                          top_p=top_p, min_p=min_p, idx=idx, logprob=logprob,
                                          err=err)
@@ -1005,7 +1002,7 @@ def vocab_sample_filtered(logits, u, *, temperature=None, top_k=None, top_p=None
         row_stride = max(row_stride, vocab)
     shape = (rows,)
     if idx is None:
-        idx = torch.empty(rows, dtype=_i32, device=dev)
+        idx = torch.empty(rows, dtype=_i32, device=logits.device)
 
     kept = []  # tensors made here live until the launch
 
@@ -1013,7 +1010,7 @@ def vocab_sample_filtered(logits, u, *, temperature=None, top_k=None, top_p=None
         if v is None:
             return 0
         if not isinstance(v, torch.Tensor):
-            v = torch.full(shape, v, dtype=dtype, device=dev)
+            v = torch.full(shape, v, dtype=dtype, device=logits.device)
             kept.append(v)
         return _need(name, v, dtype, dev, shape)
 
@@ -1022,7 +1019,7 @@ def vocab_sample_filtered(logits, u, *, temperature=None, top_k=None, top_p=None
                      per_row("top_k", top_k, _i32), per_row("top_p", top_p, _f32),
                      per_row("min_p", min_p, _f32), _need("idx", idx, _i32, dev, shape),
                      _opt("logprob", logprob, _f32, dev, shape), _opt("err", err, _i32, dev))
-    rc = lib().orthrus_vocab_sample_filtered(a, _raw_stream(dev.index))
+    rc = lib().orthrus_vocab_sample_filtered(a, _raw_stream(dev))
     if rc:
         raise OrthrusError("orthrus_vocab_sample_filtered", rc)
     return idx
