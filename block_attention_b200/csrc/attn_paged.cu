@@ -79,8 +79,13 @@ constexpr float kLazyThresh = 8.f;  // log2 units
 constexpr int kSegRing = 8;         // segments that may be alive at once
 constexpr int kFlagRing = kSegRing;
 constexpr int kSegReaders = 11;     // warps that release one: producer, Q, MMA, softmax
-constexpr int kOverhead = 2;        // a unit's start and end, in tiles
-constexpr int kMinChunk = 4;        // tiles and overheads a CTA takes at least
+// Lengths in the schedule: a tile, a wide tile, a unit's start and end, and what a
+// CTA takes at least.  Measured 2150, 3750 and 8000 cycles; with all tiles alike
+// and 2 of them for start and end, CTAs of tails ended 30 % late behind a prefix
+// of 8192 keys and 15 % early behind one of 16384 (131 -> 126 us)
+constexpr int kNarrow = 4, kWide = 7, kOverhead = 16;
+constexpr int kMinChunk = 4 * kNarrow;
+static_assert(kWide <= kMinChunk, "each of a unit's CTAs has a tile of it");
 constexpr int kMergeRows = 8;       // query rows of one merging CTA
 constexpr int kMergeWays = 4, kMergeDepth = 5;  // (attn_paged_merge)
 
@@ -172,7 +177,19 @@ __device__ __forceinline__ int tail_tiles(const PagedParams& p, int n) {
 // length of a tail unit in the schedule
 __device__ __forceinline__ int tail_cost(const PagedParams& p, int n) {
   const int T = tail_tiles(p, n);
-  return T ? T + kOverhead : 0;
+  return T ? kNarrow * T + kOverhead : 0;
+}
+
+// Lengths of the prefix units: wide ones (two row tiles), then single ones.
+__device__ __forceinline__ int wide_cost(const PagedParams& p) { return kWide * p.Kp + kOverhead; }
+__device__ __forceinline__ int single_cost(const PagedParams& p) {
+  return kNarrow * p.Kp + kOverhead;
+}
+__device__ __forceinline__ int wide_length(const PagedParams& p) {  // of them all
+  return p.Hkv * (p.Tq / 2) * wide_cost(p);
+}
+__device__ __forceinline__ int prefix_length(const PagedParams& p) {
+  return p.Kp ? wide_length(p) + p.Hkv * (p.Tq & 1) * single_cost(p) : 0;
 }
 
 struct Seg {
@@ -198,15 +215,16 @@ struct Walk {
       if (pos >= end) return false;
       int off, cost;  // position within the unit, its length
       if (pos < base) {
-        cost = p.Kp + kOverhead;
         // every kv-head's pairs of row tiles, then the single ones that are left
-        const int unit = pos / cost, pairs = p.Tq / 2;
+        const int pairs = p.Tq / 2, wide = wide_length(p);
         s.prefix = 1;
-        s.wide = unit < p.Hkv * pairs;
-        s.g = s.wide ? unit / pairs : unit - p.Hkv * pairs;
+        s.wide = pos < wide;
+        cost = s.wide ? wide_cost(p) : single_cost(p);
+        const int at = s.wide ? pos : pos - wide, unit = at / cost;
+        s.g = s.wide ? unit / pairs : unit;
         s.b = s.wide ? 2 * (unit - s.g * pairs) : p.Tq - 1;
-        s.unit = unit;
-        off = pos - unit * cost;
+        s.unit = s.wide ? unit : p.Hkv * pairs + unit;
+        off = at - unit * cost;
         s.T = s.Tc = p.Kp;
         s.n = p.P;
         s.lo = 0;
@@ -228,15 +246,17 @@ struct Walk {
         s.n = n;
         s.lo = shares(n, p.P, p.v_blk ? 0 : p.blk) ? p.P : 0;
         s.Tc = cache_tiles(s.lo, n);
-        s.T = cost - kOverhead;
+        s.T = (cost - kOverhead) / kNarrow;
         off = t;
       }
       const int len = min(cost - off, end - pos);
       pos += len;
       if (!s.prefix) t += len;
-      // the unit's first kOverhead positions carry no tile
-      s.t0 = max(0, off - kOverhead);
-      s.U = off + len - kOverhead - s.t0;
+      // the unit's first kOverhead positions carry no tile; a tile belongs to the
+      // CTA of its first position
+      const int per = s.wide ? kWide : kNarrow;
+      s.t0 = ceil_div(max(0, off - kOverhead), per);
+      s.U = ceil_div(max(0, off + len - kOverhead), per) - s.t0;
       if (s.U <= 0) continue;
       s.first = s.lo / kTile;
       return true;
@@ -262,11 +282,16 @@ __device__ __forceinline__ int v_item(int it0, int u, int U) {
 
 // --------------------------------------------------------------- main kernel
 
-// Scores of keys [k0, k0 + 32): those outside [lo, hi) -> -inf
+// Scores of keys k0 .. k0 + 31 outside [lo, hi) become -inf.  One word of flags
+// costs a select a score, and nothing where the whole warp sees every key.
 __device__ __forceinline__ void mask32(uint32_t (&sv)[32], int k0, int lo, int hi) {
+  const int a = lo - k0, b = hi - k0;
+  const uint32_t seen = (b >= 32 ? 0xffffffffu : b > 0 ? (1u << b) - 1 : 0u) &
+                        (a <= 0 ? 0xffffffffu : a < 32 ? 0xffffffffu << a : 0u);
+  if (__all_sync(0xffffffffu, seen == 0xffffffffu)) return;
 #pragma unroll
   for (int j = 0; j < 32; ++j)
-    if (k0 + j < lo || k0 + j >= hi) sv[j] = __float_as_uint(-INFINITY);
+    if (!(seen >> j & 1)) sv[j] = __float_as_uint(-INFINITY);
 }
 __device__ __forceinline__ float max32(const uint32_t (&sv)[32], float m) {
   float a = m, b = __uint_as_float(sv[0]);
@@ -326,7 +351,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, int c0, int lo, in
   constexpr int kStep = kCols < 64 ? kCols : 64;  // columns in registers at a time
   constexpr int N = kStep / 32;
   const uint32_t p_addr = s_addr + 64;
-  const bool mask = nv < c0 + kCols || lo > c0;
+  const bool mask = __any_sync(0xffffffffu, nv < c0 + kCols || lo > c0);
   uint32_t a[N][32];
   auto load = [&](int c1) {  // scores of columns [c1, c1 + kStep)
 #pragma unroll
@@ -449,7 +474,7 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
 
   // ---- the schedule: its whole length, then where this CTA's share begins.
   // The first kThreads sequences stay in registers between the two steps.
-  const int base = p.Hkv * p.Tw * (p.Kp + kOverhead);  // Tw: prefix units of a kv-head
+  const int base = prefix_length(p);
   int pos, end;
   {
     int cost0 = 0, rest = 0;
@@ -913,24 +938,29 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
           uint8_t* vt = smem + kRingOff + (vi % kSlots) * kSlotBytes;
           // rows outside the keys [lo_tile, nv_tile) hold anything: zero them,
           // and the non-finite elements of rows [fz, nv_tile)
-          for (int e = wg_tid; e < kTile * 8 * halves; e += 128) {
-            const int h = e / (kTile * 8), row = (e / 8) % kTile;
-            if (row >= lo_tile && row < min(fz, nv_tile)) continue;
-            uint4* at = reinterpret_cast<uint4*>(vt + h * kHalfTile + (e % (kTile * 8)) * 16);
-            if (row < lo_tile || row >= nv_tile) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            const uint4 v = *at;
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            bool found = false;
+          // (a thread keeps to one 16-byte column of every kRowStep-th row)
+          constexpr int kRowStep = 128 / (8 * halves);
+          const int col = wg_tid % (8 * halves), r0 = wg_tid / (8 * halves);
+          uint8_t* vc = vt + (col >> 3) * kHalfTile + (col & 7) * 16;
+          auto from = [&](int row) { return row + ((r0 - row) & (kRowStep - 1)); };
+          auto at = [&](int row) { return reinterpret_cast<uint4*>(vc + row * 128); };
+          for (int row = r0; row < lo_tile; row += kRowStep) *at(row) = make_uint4(0, 0, 0, 0);
+          for (int row = from(nv_tile); row < kTile; row += kRowStep)
+            *at(row) = make_uint4(0, 0, 0, 0);
+          const int scan = min(max(fz, lo_tile), kTile);  // (fz may be the largest int)
+          for (int row = from(scan); row < nv_tile; row += kRowStep) {
+            const uint4 v = *at(row);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w}, some = 0;
+            // an exponent of all ones carries into its half's top bit
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (nonfinite_bf16(w[i])) { w[i] &= 0xffff0000u; found = true; }
-              if (nonfinite_bf16(w[i] >> 16)) { w[i] &= 0xffffu; found = true; }
-            }
-            if (found) {
-              *at = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 4; ++i) some |= (w[i] & 0x7f807f80u) + 0x00800080u;
+            if (some & 0x80008000u) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (nonfinite_bf16(w[i])) w[i] &= 0xffff0000u;
+                if (nonfinite_bf16(w[i] >> 16)) w[i] &= 0xffffu;
+              }
+              *at(row) = make_uint4(w[0], w[1], w[2], w[3]);
               has_nf[sg % kFlagRing] = 1;
             }
           }
@@ -1152,11 +1182,11 @@ attn_paged_merge(const __grid_constant__ PagedParams p) {
   const int i = row_ok ? rt / p.G : 0;
   __nv_bfloat16* out =
       p.out + ((int64_t)(b * p.blk + i) * p.Hq + g * p.G + rt % p.G) * kD + 8 * c8;
-  const int w0 = base + p.Hkv * before + g * (T + kOverhead) + kOverhead;  // first tile
+  const int w0 = base + p.Hkv * before + g * (kNarrow * T + kOverhead) + kOverhead;  // first tile
   int t_first = 0, t_last = -1, p_first = 0, p_last = -1;
   if (T > 0) {
     t_first = w0 / chunk;
-    t_last = (w0 + T - 1) / chunk;
+    t_last = (w0 + kNarrow * (T - 1)) / chunk;
     if (!sh && t_first == t_last) return;  // written by the main kernel
   } else if (!sh) {  // no key at all
     if (row_ok && way == 0) *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
@@ -1167,11 +1197,13 @@ attn_paged_merge(const __grid_constant__ PagedParams p) {
   const int unit = single ? p.Hkv * (p.Tq / 2) + g : g * (p.Tq / 2) + tile / 2;
   const int rp = (tile & 1) * kRows + (b % p.ns) * p.rowsT;  // (a single tile's index is even)
   if (sh) {
-    const int first = unit * (p.Kp + kOverhead) + kOverhead;
+    const int first =
+        kOverhead + (single ? wide_length(p) + g * single_cost(p) : unit * wide_cost(p));
     p_first = first / chunk;
-    p_last = (first + p.Kp - 1) / chunk;
+    p_last = (first + (single ? kNarrow : kWide) * (p.Kp - 1)) / chunk;
   }
-  // pieces: the prefix's, then the tail's
+  // pieces: the prefix's, then the tail's (no CTA between a unit's first and last
+  // goes without a tile of it: kWide <= kMinChunk)
   const int np = p_last - p_first + 1, pieces = np + t_last - t_first + 1;
   auto slot_of = [&](int x) -> int64_t {
     return x < np ? unit + p_first + x : tail_slot(p, b, g, t_first + x - np, x == np);
@@ -1384,8 +1416,9 @@ int paged_tc_launch(const orthrus_paged_attn_args& a, cudaStream_t st) {
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
 
   // no more CTAs than the most tiles there can be
-  const int64_t most = (int64_t)a.Hkv * y.Tw * (y.Kp + kOverhead) +
-                       (int64_t)a.Hkv * a.B * (ceil_div(a.max_ctx, kTile) + 1 + kOverhead);
+  const int64_t most =  // (check_shape keeps it below 2^31)
+      (int64_t)a.Hkv * y.Tw * (kWide * (int64_t)y.Kp + kOverhead) +
+      (int64_t)a.Hkv * a.B * (kNarrow * ((int64_t)ceil_div(a.max_ctx, kTile) + 1) + kOverhead);
   const int64_t want = (most + kMinChunk - 1) / kMinChunk;
   int C = sms < kMaxCtas ? sms : kMaxCtas;
   if (want < C) C = (int)want;

@@ -387,9 +387,11 @@ int check_shape(const orthrus_paged_attn_args* a) {
   if (a->page_size < 16 || a->page_size > 256 || (a->page_size & (a->page_size - 1)))
     return ORTHRUS_EUNSUPPORTED;
   if ((a->k_blk != nullptr) != (a->v_blk != nullptr)) return ORTHRUS_EINVAL;
-  // grid limits, and 32-bit tile, row and slot numbers
+  // grid limits, and 32-bit tile, row and slot numbers: a sequence and kv-head are
+  // at most 10 tiles' worth in the schedule of attn_paged.cu (4 and half of 7 for
+  // every 128 keys, starts and ends)
   const int64_t tiles = a->max_ctx / 64 + 4;
-  if (a->B > 65535 || a->Hkv > 65535 || (int64_t)a->B * a->Hkv * tiles > (1 << 30) ||
+  if (a->B > 65535 || a->Hkv > 65535 || (int64_t)a->B * a->Hkv * tiles > (1 << 27) ||
       (int64_t)a->B * a->blk * a->Hq > (1 << 30) ||
       (int64_t)a->pages * a->Hkv * a->page_size > 0x7fffffffll)
     return ORTHRUS_EUNSUPPORTED;

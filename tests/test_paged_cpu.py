@@ -164,6 +164,16 @@ def test_paged_attention_refusals(L, dtype, kw, code):
     assert L.orthrus_paged_attn(ctypes.byref(a), None) == code
 
 
+@pytest.mark.parametrize("dtype,ctx,code", [(1, 64 * 16380, -3), (1, 64 * 16381, -2),
+                                            (0, 64 * 16381, -2)])
+def test_paged_attention_schedule_limit(L, dtype, ctx, code):
+    """4096 sequences and 2 kv-heads: 16380 pieces of 64 keys each fit, more do not
+    (those that fit are turned away for the workspace, which bf16 always needs)."""
+    a = filled(ba.PagedAttnArgs, **{**ATTN, "B": 4096, "max_pages": 1 << 16, "workspace": None,
+                                    "dtype": dtype, "max_ctx": ctx})
+    assert L.orthrus_paged_attn(ctypes.byref(a), None) == code
+
+
 @pytest.mark.parametrize("dtype", [0, 1])
 def test_paged_attention_workspace(L, dtype):
     a = filled(ba.PagedAttnArgs, **{**ATTN, "dtype": dtype, "max_pages": 500, "max_ctx": 8000})
