@@ -69,13 +69,18 @@ __device__ __forceinline__ int find_seq(const int32_t* starts, int B, int r) {
   return lo;
 }
 
-// Rows that sequence b appends; -1 if its counts or length are out of range.
+// Rows that sequence b appends; -1 if its counts or lengths are out of range.
 __device__ __forceinline__ int taken_rows(const RowParams& p, int b, int n) {
   int cnt = p.blk;
-  if (p.row_starts) cnt = p.row_starts[b + 1] - p.row_starts[b];
-  else if (p.n_rows) cnt = p.n_rows[b];
-  if (n < 0 || cnt < 0 || (!p.row_starts && cnt > p.blk)) return -1;
-  return cnt;
+  if (p.row_starts) {
+    const int lo = p.row_starts[b], hi = p.row_starts[b + 1];
+    if (lo < 0 || hi < lo || hi > p.rows) return -1;
+    cnt = hi - lo;
+  } else if (p.n_rows) {
+    cnt = p.n_rows[b];
+    if (cnt < 0 || cnt > p.blk) return -1;
+  }
+  return n < 0 || (int64_t)n + cnt > 0x7fffffff ? -1 : cnt;
 }
 
 struct Row {

@@ -109,8 +109,9 @@ int orthrus_rope(const orthrus_rope_args* a, orthrus_stream_t stream);
  * Nothing else is written: not the other slots of a page, not q_out rows that
  * are not taken.  A row whose position lies outside the table
  * (ORTHRUS_ECAPACITY), whose page id lies outside the pool (ORTHRUS_EINVAL),
- * or whose sequence has a negative length or an n_rows outside [0, blk]
- * (ORTHRUS_ECAPACITY) is not written.  Two rows with the same page and slot
+ * or whose sequence has a negative length, an n_rows outside [0, blk], starts
+ * outside [0, rows] or a new length above 2^31 - 1 (ORTHRUS_ECAPACITY) is not
+ * written.  Two rows with the same page and slot
  * leave one of them, or a mix.
  *
  * advance: ctx_lens[b] += rows taken, once every row has been read, for each

@@ -210,6 +210,31 @@ def test_append_refused_rows_are_skipped_and_reported():
     assert err.item() == -4 and lens.tolist() == [14, 30, 16, 4] and not kp.any()
 
 
+def test_append_refuses_starts_past_the_rows_and_lengths_past_32_bits():
+    """Starts beyond the rows given, and lengths beyond 2^31 - 1, neither write
+    nor advance."""
+    dev = dict(dtype=torch.int32, device="cuda")
+
+    def run(starts, lens, ps, cols):
+        k = torch.ones(6, 1, 4, device="cuda")
+        pool = torch.zeros(2, 3, 1, ps, 4, device="cuda")
+        err = torch.zeros(1, **dev)
+        ctx = torch.tensor(lens, **dev)
+        table = torch.arange(3, **dev)[:, None].expand(3, cols).contiguous()
+        ba.paged_append(k, k, pool[0], pool[1], table, ctx, row_starts=torch.tensor(starts, **dev),
+                        advance=True, err=err)
+        return ctx.tolist(), err.item(), [int(n) // 4 for n in pool[0].sum((1, 2, 3))]
+
+    assert run([0, 2, 4, 6], [1, 2, 3], 16, 1) == ([3, 4, 5], 0, [2, 2, 2])
+    # the last sequence's end is not there
+    assert run([0, 2, 4, 9], [1, 2, 3], 16, 1) == ([3, 4, 3], -4, [2, 2, 0])
+    lens, err, slots = run([0, 4, 2, 6], [1, 2, 3], 16, 1)  # a negative count
+    assert lens[1] == 2 and slots[1] == 0
+    top = 2 ** 31 - 1
+    got = run([0, 2, 4, 6], [top - 1, 0, top - 2], 1 << 16, 1 << 15)
+    assert got == ([top - 1, 2, top], -4, [0, 2, 2])
+
+
 # ---------------------------------------------------------------- attention
 
 class Attn:
