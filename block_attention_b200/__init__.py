@@ -753,9 +753,24 @@ class _StreamWorkspace(Workspace):
         return self.buf
 
 
+class _CaptureWorkspace:
+    """Scratch of one call that is being captured: from the graph's own memory,
+    so that no other graph and no eager call works in it.  Only the append's
+    ticket has to start at zero."""
+
+    def __init__(self, index, op):
+        self.device = torch.device("cuda", index)
+        self.make = torch.zeros if op == "paged_append" else torch.empty
+
+    def get(self, nbytes: int) -> torch.Tensor:
+        return self.make(nbytes, dtype=torch.uint8, device=self.device)
+
+
 def _stream_ws(ws, index, op):
     """Caller's workspace, else the current stream's default for this op."""
     if ws is None:
+        if torch.cuda.is_current_stream_capturing():
+            return _CaptureWorkspace(index, op)
         key = (index, op, _raw_stream(index))
         ws = _default_ws.get(key)
         if ws is None:

@@ -480,6 +480,37 @@ def test_attention_captured_with_changing_lengths_and_two_streams():
     assert all(torch.equal(o, out) for o in got)
 
 
+def test_graphs_replayed_at_once_share_no_scratch():
+    """Captured without a workspace of their own: two graphs of append (with its
+    ticket) and split attention, replayed on two streams together."""
+    sets = []
+    for seed in (21, 22):
+        a = Attn("bf16", 128, 8, 2, 8, False, True, 32, [2000, 1500, 700], 0, seed=seed)
+        d = [None if t is None else t.cuda() for t in (a.q, a.kb, a.vb, a.k, a.v, a.table)]
+        lens = torch.tensor(a.lens, dtype=torch.int32).cuda()
+        count, none = lens.clone(), torch.zeros_like(lens)
+        out = torch.empty_like(d[0])
+        ref = ba.paged_block_attn(*d, lens, ba.CAUSAL_VERIFY, max_ctx=a.max_ctx)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(4):
+                # no rows are taken, so the pools and the lengths stay
+                ba.paged_append(d[1], d[2], d[3], d[4], d[5], count, n_rows=none, advance=True)
+                ba.paged_block_attn(*d, lens, ba.CAUSAL_VERIFY, max_ctx=a.max_ctx, out=out)
+        sets.append((graph, out, ref, d, lens, count, none, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(25):
+        for s in sets:
+            s[1].zero_()
+        torch.cuda.synchronize()
+        for s in sets:
+            with torch.cuda.stream(s[-1]):
+                s[0].replay()
+        torch.cuda.synchronize()
+        for _, out, ref, _, lens, count, _, _ in sets:
+            assert torch.equal(out, ref) and torch.equal(count, lens)
+
+
 def test_append_then_attention_matches_the_dense_cache():
     """A prefill in two ragged pieces, a decoding step and a round's verify view
     over pages, against the same keys in a dense cache."""
