@@ -26,13 +26,16 @@
 // tile order, so the result depends on the lengths only, not on timing.
 //
 // Per CTA (12 warps):
-//   warp 0       K/V producer: a ring of five 32 KB slots, filled in the order
-//                the tiles are used (K0 K1 V0 K2 V1 ..); each lane loads one
-//                page's rows of one 64-dim half, the page ids two tiles ahead
+//   warps 0, 3   K tiles; Q and V tiles.  K and V go into a ring of five 32 KB
+//                slots in the order they are used (K0 K1 V0 K2 V1 ..); each lane
+//                loads one page's rows of one 64-dim half, the page ids two tiles
+//                ahead.  A load takes its warp 75 cycles: one warp for K and V
+//                bound batches with small pages (32 loads a tile at 16 rows: 16
+//                ragged sequences took 265 us, now 202; one sequence of 8192
+//                keys, all start and end, 19.6 and now 21.0)
 //   warp 1       MMA issuer (one thread)
 //   warp 2       walks the schedule ahead of the others and hands its units out
 //                through a ring in shared memory
-//   warp 3       Q tiles
 //   warps 4..11  softmax, two warpgroups X = 0, 1; a wide unit's row tile X
 //                belongs to warpgroup X, otherwise they take turns on the tiles
 // S(u) = Q K(u)^T goes to the warpgroup's own 128 TMEM columns; P(u) replaces
@@ -78,7 +81,7 @@ constexpr int kOCol = 256;
 constexpr float kLazyThresh = 8.f;  // log2 units
 constexpr int kSegRing = 8;         // segments that may be alive at once
 constexpr int kFlagRing = kSegRing;
-constexpr int kSegReaders = 11;     // warps that release one: producer, Q, MMA, softmax
+constexpr int kSegReaders = 11;     // warps that release one: K, V, MMA, softmax
 // Lengths in the schedule: a tile, a wide tile, a unit's start and end, and what a
 // CTA takes at least.  Measured 2150, 3750 and 8000 cycles; with all tiles alike
 // and 2 of them for start and end, CTAs of tails ended 30 % late behind a prefix
@@ -590,12 +593,13 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
           if (!more) break;
         }
       }
-    } else if (warp == 0) {
-      // ================================================== K/V producer
+    } else if (warp != 1) {
+      // ================================================== K (warp 0), Q and V (warp 3)
+      const bool is_v = warp == 3;
       const int box = min(p.page_size, kTile);  // rows of one box
       const int npg = kTile / box;              // pages a tile touches at most
       const int mh = lane / npg, mi = lane % npg;  // this lane's half and page of a tile
-      int it = 0;  // items issued by this CTA so far
+      int last[3] = {-1, -1, -1};  // items issued last: of five in a row one warp has 3 at most
       bool stop = false;
       Seg s{}, nx{};
       // first key of this lane's box of unit tile t, whether it holds keys, its page
@@ -610,8 +614,8 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
                              box_key(s, t) / p.page_size]
                    : -1;
       };
-      // one K or V tile of segment sg into the next slot
-      auto issue = [&](int sg, bool is_v, int t, int id) {
+      // tile t of segment sg into item it's slot
+      auto issue = [&](int sg, int t, int id, int it) {
         const uint32_t bar = bars.full(it % kSlots), dst = slot_s(it);
         if (__any_sync(full_mask, *abort_flag != 0) ||
             !__all_sync(full_mask,
@@ -647,7 +651,9 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
                              64 * mh,
                              (id * p.Hkv + s.g) * p.page_size + box_key(s, t) % p.page_size);
         }
-        ++it;
+        last[0] = last[1];
+        last[1] = last[2];
+        last[2] = it;
       };
       // the page ids of the next two tiles, and those of the next segment's first
       // ones, travel while this tile waits for its slot
@@ -658,57 +664,57 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
         id1 = page_of(s, s.t0 + 1);
         id2 = page_of(s, s.t0 + 2);
       }
+      int it0 = 0, nq = 0;  // items before the segment; Q tiles requested
       for (int sg = 0; more && !stop; ++sg) {
-        const int t1 = s.t0 + s.U;
-        issue(sg, false, s.t0, id0);
-        const bool more2 = seg_copy(sg + 1, nx);
+        bool more2 = false;
         int n0 = -1, n1 = -1, n2 = -1;
-        if (more2) {
-          n0 = page_of(nx, nx.t0);
-          n1 = page_of(nx, nx.t0 + 1);
-          n2 = page_of(nx, nx.t0 + 2);
+        if (is_v) {
+          if (__any_sync(full_mask, *abort_flag != 0) ||
+              (sg > 0 && !__all_sync(full_mask, ptx::mbar_wait(bars.q_free(), (sg - 1) & 1)))) {
+            if (!*abort_flag) record_timeout(p.err, abort_flag);
+            break;
+          }
+          if (lane == 0) {
+            const int rows = s.prefix ? p.ns * p.rowsT : p.rowsT;
+            const int reps = s.prefix ? 1 + s.wide : p.copies;
+            ptx::mbar_expect_tx(bars.q_full(), (uint32_t)(halves * reps * rows * 128));
+            for (int i = 0; i < reps; ++i) {
+              const uint32_t dst = q_s + (s.prefix ? i * kQBytes : i * (kRows / p.copies) * 128);
+              const int b0 = s.prefix ? (s.b + i) * p.ns : s.b;
+              for (int h = 0; h < halves; ++h)
+                ptx::tma_load_3d(dst + h * (kRows * 128), s.prefix ? &p.tm_qp : &p.tm_q,
+                                 bars.q_full(), 64 * h, s.g * p.G, b0 * p.blk);
+            }
+          }
+          __syncwarp();
+          ++nq;
         }
-        for (int t = s.t0; t < t1 && !stop; ++t) {
-          const int id3 = page_of(s, t + 3);
-          if (t + 1 < t1) issue(sg, false, t + 1, id1);
-          if (!stop) issue(sg, true, t, id0);
+        for (int u = 0; u < s.U && !stop; ++u) {
+          const int id3 = page_of(s, s.t0 + u + 3);
+          issue(sg, s.t0 + u, id0, is_v ? v_item(it0, u, s.U) : k_item(it0, u));
           id0 = id1; id1 = id2; id2 = id3;
+          if (u > 0) continue;
+          more2 = seg_copy(sg + 1, nx);
+          if (more2) {
+            n0 = page_of(nx, nx.t0);
+            n1 = page_of(nx, nx.t0 + 1);
+            n2 = page_of(nx, nx.t0 + 2);
+          }
         }
+        it0 += 2 * s.U;
         more = more2;
         s = nx;
         id0 = n0; id1 = n1; id2 = n2;
       }
-      // every issued load must have landed before the CTA exits
-      for (int x = max(0, it - kSlots); x < it; ++x)
-        if (!ptx::mbar_wait(bars.full(x % kSlots), (x / kSlots) & 1))
+      // every issued load must have landed before the CTA exits (an item whose slot
+      // has been filled again has)
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (last[i] >= max(0, stop ? 0 : it0 - kSlots) &&
+            !ptx::mbar_wait(bars.full(last[i] % kSlots), (last[i] / kSlots) & 1))
           record_timeout(p.err, abort_flag);
-    } else if (warp == 3) {
-      // ================================================== Q tiles
-      Seg s;
-      int sg = 0;
-      for (; seg_copy(sg, s); ++sg) {
-        if (__any_sync(full_mask, *abort_flag != 0) ||
-            (sg > 0 && !__all_sync(full_mask, ptx::mbar_wait(bars.q_free(), (sg - 1) & 1)))) {
-          if (!*abort_flag) record_timeout(p.err, abort_flag);
-          break;
-        }
-        if (lane == 0) {
-          const int rows = s.prefix ? p.ns * p.rowsT : p.rowsT;
-          const int reps = s.prefix ? 1 + s.wide : p.copies;
-          ptx::mbar_expect_tx(bars.q_full(), (uint32_t)(halves * reps * rows * 128));
-          for (int i = 0; i < reps; ++i) {
-            const uint32_t dst = q_s + (s.prefix ? i * kQBytes : i * (kRows / p.copies) * 128);
-            const int b0 = s.prefix ? (s.b + i) * p.ns : s.b;
-            for (int h = 0; h < halves; ++h)
-              ptx::tma_load_3d(dst + h * (kRows * 128), s.prefix ? &p.tm_qp : &p.tm_q,
-                               bars.q_full(), 64 * h, s.g * p.G, b0 * p.blk);
-          }
-        }
-        __syncwarp();
-      }
-      if (sg > 0 && !ptx::mbar_wait(bars.q_full(), (sg - 1) & 1))
-        record_timeout(p.err, abort_flag);
-    } else if (warp == 1) {
+      if (nq > 0 && !ptx::mbar_wait(bars.q_full(), (nq - 1) & 1)) record_timeout(p.err, abort_flag);
+    } else {
       // ================================================== MMA issuer
       // The whole warp walks and waits, so that descriptors and addresses stay
       // warp-uniform; one elected lane issues.
