@@ -342,76 +342,69 @@ __device__ __forceinline__ float raise_max(RowState& st, float ms, bool& any) {
   return f;
 }
 
-// Softmax of one tile for the row of this thread: kCols keys from column c0 of
-// the tile, of which the row sees [lo, nv).  Reads S, rescales O (if it holds
-// anything) and writes P, zero in the other columns.  With a barrier `early` (whole
-// tiles of one copy only) P of keys 64.. is announced on it as soon as it is there,
-// so that its product with V runs under the exponentials of the rest.
-template <int kCols, int kD>
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, int c0, int lo, int nv, float c,
-                                             bool row_ok, RowState& st, uint32_t o_addr,
+// Softmax of one tile for the row of this thread: `cols` keys (32, 64 or 128) from
+// column c0 of the tile, of which the row sees [lo, nv).  Reads S, rescales O (if it
+// holds anything) and writes P, zero in the other copies' columns.  With a barrier
+// `early` (whole tiles of one copy only) P of keys 64.. is announced on it as soon
+// as it is there, so that its product with V runs under the exponentials of the
+// rest.  32 columns a turn, one loop for every number of them: the code of all
+// roles has to share the instruction cache (loops of 64 columns for whole tiles
+// beside shorter ones: 118 us for 128 requests behind a 16k prefix, this 109; 98
+// and 102 for 16 verify blocks behind 8k; with the next columns' loads under way
+// 137 and 111).
+template <int kD>
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, int c0, int cols, int lo, int nv,
+                                             float c, bool row_ok, RowState& st, uint32_t o_addr,
                                              bool has_o, uint32_t early) {
-  constexpr int kStep = kCols < 64 ? kCols : 64;  // columns in registers at a time
-  constexpr int N = kStep / 32;
   const uint32_t p_addr = s_addr + 64;
-  const bool mask = __any_sync(0xffffffffu, nv < c0 + kCols || lo > c0);
-  uint32_t a[N][32];
-  auto load = [&](int c1) {  // scores of columns [c1, c1 + kStep)
-#pragma unroll
-    for (int h = 0; h < N; ++h) ptx::tmem_ld32(s_addr + c1 + 32 * h, a[h]);
-    ptx::tmem_wait_ld();
-    if (mask)
-#pragma unroll
-      for (int h = 0; h < N; ++h) mask32(a[h], c1 + 32 * h, lo, nv);
+  const bool mask = __any_sync(0xffffffffu, nv < c0 + cols || lo > c0);
+  uint32_t a[32];
+  auto load = [&](int c1) {  // scores of columns [c1, c1 + 32)
+    ptx::tmem_ld32_sync(s_addr + c1, a);
+    if (mask) mask32(a, c1, lo, nv);
   };
   float mt = -INFINITY;
 #pragma unroll 1
-  for (int c1 = c0; c1 < c0 + kCols; c1 += kStep) {
+  for (int c1 = c0; c1 < c0 + cols; c1 += 32) {
     load(c1);
-#pragma unroll
-    for (int h = 0; h < N; ++h) mt = max32(a[h], mt);
+    mt = max32(a, mt);
   }
   bool rescale;
   const float f = raise_max(st, row_ok ? mt * c : -INFINITY, rescale);
   if (rescale && has_o) {
 #pragma unroll 1
     for (int cb = 0; cb < kD; cb += 32) {
-      ptx::tmem_ld32_sync(o_addr + cb, a[0]);
+      ptx::tmem_ld32_sync(o_addr + cb, a);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) a[0][j] = __float_as_uint(__uint_as_float(a[0][j]) * f);
-      ptx::tmem_st32(o_addr + cb, a[0]);
+      for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
+      ptx::tmem_st32(o_addr + cb, a);
     }
-    if (kCols == kStep) load(c0);
   }
   const float nm = st.m == -INFINITY ? 0.f : -st.m;
   const uint64_t c2 = ptx::pack2(c, c), nm2 = ptx::pack2(nm, nm);
   uint64_t ls[2] = {0, 0};
-  if constexpr (kCols < kTile) {  // the other copies' keys: weight zero
+  // From the last columns down: P's words of keys 64.. replace S's columns 96..,
+  // which are in registers by then, those of keys 0.. the columns 64..95.  Read
+  // again rather than kept: fewer registers.
+#pragma unroll 1
+  for (int c1 = c0 + cols - 32; c1 >= c0; c1 -= 32) {
+    load(c1);
+    uint32_t w[16];
+    exp32(a, c2, nm2, ls, w);
+    ptx::tmem_st16(p_addr + c1 / 2, w);
+    if (c1 == kTile / 2 && early) {
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(early);
+    }
+  }
+  if (cols < kTile) {  // the other copies' keys: weight zero
     uint32_t zero[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) zero[j] = 0;
 #pragma unroll
     for (int g = 0; g < 4; ++g)
-      if (g < c0 / 32 || g >= (c0 + kCols) / 32) ptx::tmem_st16(p_addr + 16 * g, zero);
-  }
-  // From the last columns down: P's words of keys 64.. replace S's columns 96..,
-  // which are in registers by then, those of keys 0.. the columns 64..95.  Read
-  // again rather than kept: fewer registers, and a loop of half the code.
-#pragma unroll 1
-  for (int c1 = c0 + kCols - kStep; c1 >= c0; c1 -= kStep) {
-    if (kCols > kStep) load(c1);
-    uint32_t w[16 * N];
-#pragma unroll
-    for (int h = 0; h < N; ++h) exp32(a[h], c2, nm2, ls, w + 16 * h);
-    if constexpr (N == 2)
-      ptx::tmem_st32(p_addr + c1 / 2, w);
-    else
-      ptx::tmem_st16(p_addr + c1 / 2, w);
-    if (kCols == 128 && c1 > 0 && early) {
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(early);
-    }
+      if (g < c0 / 32 || g >= (c0 + cols) / 32) ptx::tmem_st16(p_addr + 16 * g, zero);
   }
   float l0, l1;
   ptx::unpack2(ptx::add2(ls[0], ls[1]), l0, l1);
@@ -923,13 +916,8 @@ attn_paged_kernel(const __grid_constant__ PagedParams p) {
           const float sc = p.scale_log2;
           const uint32_t o_addr = lane_addr + kOCol + X * kD;
           const bool has_o = done > 0;  // O holds this warpgroup's earlier tiles
-          if (copies == 1)
-            softmax_tile<128, kD>(s_addr, 0, lo_tile, nv, sc, row_ok, st, o_addr, has_o,
-                                  early ? bars.p_high(X) : 0u);
-          else if (copies == 2)
-            softmax_tile<64, kD>(s_addr, c0, lo_tile, nv, sc, row_ok, st, o_addr, has_o, 0u);
-          else
-            softmax_tile<32, kD>(s_addr, c0, lo_tile, nv, sc, row_ok, st, o_addr, has_o, 0u);
+          softmax_tile<kD>(s_addr, c0, span, lo_tile, nv, sc, row_ok, st, o_addr, has_o,
+                           early ? bars.p_high(X) : 0u);
           ptx::tmem_wait_st();
         } else if (early) {
           ptx::mbar_arrive(bars.p_high(X));
