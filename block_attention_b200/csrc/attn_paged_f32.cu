@@ -24,6 +24,12 @@
 //
 // Keys of the shared prefix are looked up through row 0 of the page table;
 // FP32 reads them once a sequence.
+//
+// Measured: 2 sequences of 700 to 2048 keys, 32 rows, 16 query and 8 kv-heads x
+// 128: 48.6 us a call, 8 of them the merge; the products at the FP32 pipe's rate
+// take 11.6.  Bound by tiles that a CTA takes one after the other with its barriers
+// (two or three for each SM), and by the shared-memory vectors beside the
+// multiply-adds.
 #include <math.h>
 
 #include "attn_paged.cuh"
