@@ -10,7 +10,9 @@
 // over (row groups, column groups): a thread owns RPT rows, four keys of each
 // score tile and D/16 dims of the output, so a step of four dims costs
 // RPT + 4 shared-memory vectors for 16 RPT multiply-adds and the FP32 pipe, not
-// shared memory, bounds the tile products.  Q, K, V and P rows are padded by
+// shared memory, bounds the tile products.  Multiply-adds go two to an instruction:
+// neighbouring dims of a score's sum (even and odd ones added up apart, whatever
+// RPT) and of the output.  Q, K, V and P rows are padded by
 // four floats, which spreads the vectors of a column group over all banks.
 // P takes K's place once the scores are taken, so that two CTAs of up to 64 rows
 // share an SM and one's loads (cp.async; each key's row is looked up once, a
@@ -157,29 +159,36 @@ __global__ void __launch_bounds__(kThreads, RPT < 8 ? 2 : 1) f32_kernel(const F3
     __syncthreads();
     // ---- scores: rows ty*RPT.., keys tx + 16 j (a column group's key rows
     // lie 16 apart, so that their vectors fall into different banks)
+    uint64_t s2[RPT][4];  // sums over even and over odd dims
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s2[i][j] = 0;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+      ulonglong2 kf[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        kf[j] = *reinterpret_cast<const ulonglong2*>(Ks + (tx + 16 * j) * kLd + d);
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const ulonglong2 qf = *reinterpret_cast<const ulonglong2*>(Qs + (ty * RPT + i) * kLd + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s2[i][j] = ptx::fma2(qf.x, kf[j].x, s2[i][j]);
+          s2[i][j] = ptx::fma2(qf.y, kf[j].y, s2[i][j]);
+        }
+      }
+    }
     float s[RPT][4];
 #pragma unroll
     for (int i = 0; i < RPT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < D; d += 4) {
-      float4 kf[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        kf[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * kLd + d);
-#pragma unroll
-      for (int i = 0; i < RPT; ++i) {
-        const float4 qf = *reinterpret_cast<const float4*>(Qs + (ty * RPT + i) * kLd + d);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[i][j] = fmaf(qf.x, kf[j].x, s[i][j]);
-          s[i][j] = fmaf(qf.y, kf[j].y, s[i][j]);
-          s[i][j] = fmaf(qf.z, kf[j].z, s[i][j]);
-          s[i][j] = fmaf(qf.w, kf[j].w, s[i][j]);
-        }
+      for (int j = 0; j < 4; ++j) {
+        float even, odd;
+        ptx::unpack2(s2[i][j], even, odd);
+        s[i][j] = even + odd;
       }
-    }
     __syncthreads();  // K is read: P may replace it
     // ---- softmax of the tile, row by row over the 16 threads of a row group
 #pragma unroll
@@ -225,15 +234,15 @@ __global__ void __launch_bounds__(kThreads, RPT < 8 ? 2 : 1) f32_kernel(const F3
         for (int jj = 0; jj < 4; ++jj) {
 #pragma unroll
           for (int d = 0; d < kDims / 4; ++d) {
-            const float4 vf =
-                *reinterpret_cast<const float4*>(Vs + (j + jj) * kLd + 4 * tx + 64 * d);
+            const ulonglong2 vf =
+                *reinterpret_cast<const ulonglong2*>(Vs + (j + jj) * kLd + 4 * tx + 64 * d);
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
               const float w = jj == 0 ? pf[i].x : jj == 1 ? pf[i].y : jj == 2 ? pf[i].z : pf[i].w;
-              o[i][4 * d] = fmaf(w, vf.x, o[i][4 * d]);
-              o[i][4 * d + 1] = fmaf(w, vf.y, o[i][4 * d + 1]);
-              o[i][4 * d + 2] = fmaf(w, vf.z, o[i][4 * d + 2]);
-              o[i][4 * d + 3] = fmaf(w, vf.w, o[i][4 * d + 3]);
+              const uint64_t w2 = ptx::pack2(w, w);
+              float* at = &o[i][4 * d];
+              ptx::unpack2(ptx::fma2(w2, vf.x, ptx::pack2(at[0], at[1])), at[0], at[1]);
+              ptx::unpack2(ptx::fma2(w2, vf.y, ptx::pack2(at[2], at[3])), at[2], at[3]);
             }
           }
         }
