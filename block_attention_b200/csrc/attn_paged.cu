@@ -63,8 +63,8 @@
 //   64 sequences of up to 8192 keys, one row, 32-row pages       170 (164, bytes)
 //   16 sequences of 1k to 32k keys, 32 rows, 16-row pages        203 (176, bytes)
 //   one sequence of 8192 keys, 32 rows                           20.6 (5.2, bytes)
-//   16 sequences behind 8192 common keys, 32 rows                100 (45, products)
-//   128 sequences behind 16384 common keys, one row              108 (31, bytes)
+//   16 sequences behind 8192 common keys, 32 rows                101 (45, products)
+//   128 sequences behind 16384 common keys, one row              101 (31, bytes)
 // The first two are bound by HBM.  The third is two launches, a first load, five
 // tiles and a merge one after the other.  The last two are bound by the softmax
 // warps: a wide tile's 256 rows take them 3750 cycles (its products 1024, its
@@ -97,10 +97,12 @@ constexpr int kSegRing = 8;         // segments that may be alive at once
 constexpr int kFlagRing = kSegRing;
 constexpr int kSegReaders = 11;     // warps that release one: K, V, MMA, softmax
 // Lengths in the schedule: a tile, a wide tile, a unit's start and end, and what a
-// CTA takes at least.  Measured 2150, 3750 and 8000 cycles; with all tiles alike
-// and 2 of them for start and end, CTAs of tails ended 30 % late behind a prefix
-// of 8192 keys and 15 % early behind one of 16384 (131 -> 126 us)
-constexpr int kNarrow = 4, kWide = 7, kOverhead = 16;
+// CTA takes at least.  Measured 2150, 3750 to 4150 and 6200 (row copies) to 8000
+// cycles.  16 verify blocks behind 8k and 128 requests behind a 16k prefix take, at
+// wide / overhead 7 / 16: 101 and 109 us, 7 / 12: 101 and 101, 8 / 12: 108 and 99,
+// 9 / 16: 108 and 98; with wide tiles like narrow ones the tails' CTAs end a third
+// after the others
+constexpr int kNarrow = 4, kWide = 7, kOverhead = 12;
 constexpr int kMinChunk = 4 * kNarrow;
 static_assert(kWide <= kMinChunk, "each of a unit's CTAs has a tile of it");
 constexpr int kMergeRows = 8;       // query rows of one merging CTA
