@@ -60,10 +60,10 @@
 //
 // Measured, 32 query and 8 kv-heads x 128, us a call (and the time of its bytes at
 // the copy rate or its products at the matrix rate):
-//   64 sequences of up to 8192 keys, one row, 32-row pages       170 (164, bytes)
-//   16 sequences of 1k to 32k keys, 32 rows, 16-row pages        203 (176, bytes)
-//   one sequence of 8192 keys, 32 rows                           20.6 (5.2, bytes)
-//   16 sequences behind 8192 common keys, 32 rows                101 (45, products)
+//   64 sequences of up to 8192 keys, one row, 32-row pages       168 (164, bytes)
+//   16 sequences of 1k to 32k keys, 32 rows, 16-row pages        204 (176, bytes)
+//   one sequence of 8192 keys, 32 rows                           20.7 (5.2, bytes)
+//   16 sequences behind 8192 common keys, 32 rows                99 (45, products)
 //   128 sequences behind 16384 common keys, one row              101 (31, bytes)
 // The first two are bound by HBM.  The third is two launches, a first load, five
 // tiles and a merge one after the other.  The last two are bound by the softmax

@@ -28,10 +28,11 @@
 // FP32 reads them once a sequence.
 //
 // Measured: 2 sequences of 700 to 2048 keys, 32 rows, 16 query and 8 kv-heads x
-// 128: 48.6 us a call, 8 of them the merge; the products at the FP32 pipe's rate
-// take 11.6.  Bound by tiles that a CTA takes one after the other with its barriers
-// (two or three for each SM), and by the shared-memory vectors beside the
-// multiply-adds.
+// 128: 46.2 us a call, 8 of them the merge; the products at the FP32 pipe's rate
+// take 11.6.  A CTA starts for 4 us (length, page ids, first rows) and takes 8 us
+// for each of its two tiles, 13 beside another on its SM: twice what the FMA pipe
+// needs, for the shared-memory vectors.  With one tile a CTA the call took 55 us
+// (starts, and twice the pieces to merge).
 #include <math.h>
 
 #include "attn_paged.cuh"

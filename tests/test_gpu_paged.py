@@ -352,6 +352,13 @@ def test_attention(dt, case):
     Attn(dt, D, Hq, Hkv, blk, in_cache, causal, ps, lens, P, seed=case).check()
 
 
+@pytest.mark.parametrize("P", [0, 40])
+def test_attention_more_sequences_than_a_cta_has_threads(P):
+    """The schedule of the first 384 sequences and of the others, summed in two steps."""
+    lens = [(37 * i) % 150 for i in range(801)]
+    Attn("bf16", 64, 2, 1, 1, True, True, 32, lens, P, seed=31).check()
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_attention_long_and_loose_bound(dt):
     """Several splits of one sequence, with a length bound far above the lengths."""
