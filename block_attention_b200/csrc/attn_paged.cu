@@ -148,7 +148,7 @@ struct __align__(64) PagedParams {
   float* o_p;     // their O, [slot][D/4][256][4]
   float2* ml_t;   // the same of the tail partials, rows per slot = G*blk
   float* o_t;
-  int B, Hq, Hkv, G, blk, rowsT, copies, ns, Tq, Tw, Kp, P;
+  int B, Hq, Hkv, G, blk, rowsT, copies, ns, Tq, Kp, P;
   int page_size, pages, max_pages, max_ctx, causal;
   float scale_log2;
 };
@@ -1420,7 +1420,7 @@ int paged_tc_launch(const orthrus_paged_attn_args& a, cudaStream_t st) {
   p.o_t = reinterpret_cast<float*>(ws + y.o_t);
   p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = G; p.blk = a.blk; p.rowsT = G * a.blk;
   p.copies = p.rowsT <= kRows / 4 ? 4 : p.rowsT <= kRows / 2 ? 2 : 1;
-  p.ns = y.ns; p.Tq = y.Tq; p.Tw = y.Tw; p.Kp = y.Kp; p.P = a.shared_prefix;
+  p.ns = y.ns; p.Tq = y.Tq; p.Kp = y.Kp; p.P = a.shared_prefix;
   p.page_size = a.page_size; p.pages = a.pages; p.max_pages = a.max_pages;
   p.max_ctx = a.max_ctx; p.causal = a.mask_mode == ORTHRUS_CAUSAL_VERIFY;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
